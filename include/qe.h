@@ -250,6 +250,17 @@ QE_API qe_status qe_linear_forward(const qe_layer_desc* desc, const qe_layer_wei
                             size_t workspace_bytes, void* stream);
 
 /*
+ * The same forward for rows that are already quantized: codes (device) int8 [T, d_in] and sa (device)
+ * fp32 [T] in token order, as qe_add_rmsnorm_quant and qe_act_quant write them for this layer's s_inv
+ * and a_bits. The routing launch copies them to their bucket positions and does not quantize; X is read
+ * for the adapters and the router. With qe_act_quant's codes of X the result is qe_linear_forward's,
+ * bit for bit. Codes lie in [-127, 127] (A8) or [-31, 31] (A6). a_bits = 16 -> QE_ERR_UNSUPPORTED.
+ */
+QE_API qe_status qe_linear_forward_codes(const qe_layer_desc* desc, const qe_layer_weights* weights, const void* X,
+                                         qe_dtype x_dtype, const int8_t* codes, const float* sa, int32_t T, void* Y,
+                                         qe_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The same forward split into its steps, for per-step timing: `stages` is a
  * bitmask of QE_STAGE_* run in the documented order. Running every stage in
  * separate calls on one stream, with the same workspace, computes exactly
@@ -376,6 +387,86 @@ QE_API qe_status qe_split_channels(const int32_t* hist, int32_t d_in, int32_t k,
 QE_API qe_status qe_cooccurrence_npmi(const int32_t* idx, int32_t T, int32_t k, const int32_t* channel_pos,
                                       int32_t d_in, int32_t C, int32_t* O, float* S, float threshold,
                                       void* stream);
+
+/* ---------------------------------------------------------------- norm and 4-bit floating point */
+
+/*
+ * The residual's addition and the root-mean-square norm in front of a quantized projection, with the
+ * normed row quantized in the same pass over it (a library operator; the paper has no counterpart).
+ *   X            (device) [T, d], fp32 or bf16
+ *   residual     (device) [T, d] in X's type, may be NULL (nothing is added)
+ *   gamma        (device) [d], fp32 or bf16 (gamma_dtype)
+ *   s_inv        (device) fp32 [d], may be NULL: the smoothing factors of the projection
+ *   residual_out (device) out [T, d] in X's type, may be NULL (and is when residual is): x + r
+ *   Y            (device) out [T, d] in X's type, may be NULL: the normed row
+ *   a_bits       8 or 6: codes int8 [T, d] and scales fp32 [T], as qe_act_quant writes them;
+ *                4: codes and scales in MXFP4 (qe_mx4_quantize); 16: no quantized output (codes and
+ *                scales are not read and may be NULL; Y or residual_out is then required).
+ * Per row: h = fl32(x + r); rstd = fl32(1 / sqrt(sum h^2 / d + eps)) with the sum, root and quotient in
+ * fp64; y = fl32(fl32(h * rstd) * gamma); the quantizers read fl32(y * s_inv), not the rounded Y. A row
+ * with a NaN or an infinity gets the scale NaN and codes 0 (int8), or NaN blocks (MXFP4).
+ * residual_out may be X or residual, and Y may be X, in place; no other output may overlap an input.
+ * Limits: d a multiple of 8 (of 32 for a_bits = 4) and <= 32768, else QE_ERR_UNSUPPORTED; T <= 1<<20;
+ * eps >= 0. T = 0 is a no-op.
+ */
+QE_API qe_status qe_add_rmsnorm_quant(const void* X, qe_dtype x_dtype, const void* residual, const void* gamma,
+                                      qe_dtype gamma_dtype, double eps, int32_t T, int32_t d, const float* s_inv,
+                                      int32_t a_bits, void* residual_out, void* Y, void* codes, void* scales,
+                                      void* stream);
+
+/*
+ * The values of per-token int8 codes (qe_act_quant, qe_add_rmsnorm_quant): out[t][k] = codes[t][k]*sa[t],
+ * fp32, or rounded once to bf16. d_in a multiple of 8.
+ */
+QE_API qe_status qe_act_dequant(const int8_t* codes, const float* sa, int32_t T, int32_t d_in, void* out,
+                                qe_dtype out_dtype, void* stream);
+
+/*
+ * MXFP4 (the OCP microscaling format with 4-bit elements), for weights [d_out, d_in] and activations
+ * [T, d_in]: 32 consecutive channels of a row share a power-of-two scale.
+ *   codes  (device) qe_mx4_code_bytes(rows, cols) bytes: row-major [rows][cols/2], the even channel in the
+ *          low nibble; E2M1: bit 3 the sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales (device) qe_mx4_scale_bytes(rows, cols) bytes: E8M0, byte = E + 127, 255 = NaN. Tiles of 128 rows
+ *          x 128 channels, 512 bytes each, tile (row/128, col/128) at (row/128 * ceil(cols/128) + col/128)*512;
+ *          the scale of (row, block b = col/32) is byte (row%32)*16 + (row%128)/32*4 + b%4 of its tile.
+ *          Blocks past cols hold 127. Bytes of rows past the last are not written and reach no output.
+ * Limits: cols a multiple of 32 (else QE_ERR_INVALID_ARG) and <= 1<<20, rows <= 1<<24.
+ */
+QE_API size_t qe_mx4_code_bytes(int32_t rows, int32_t cols);  /* 0 on an invalid shape */
+QE_API size_t qe_mx4_scale_bytes(int32_t rows, int32_t cols); /* 0 on an invalid shape */
+
+/*
+ * Quantizes v = fl32(x * s[col]) (s NULL: v = x), X fp32 or bf16 [rows, cols]. Per block: E = floor(log2 max|v|) - 2,
+ * kept in [-127, 127]; code = v * 2^-E rounded to the nearest E2M1 value, ties to even, magnitudes beyond 6
+ * to 6. A block of zeros gets E = -127; one with a NaN or an infinity the scale NaN and codes 0.
+ * s_inv (device) out, fp32 [cols] = fl32(1/s), the factors of a layer's activations; may be NULL, and is
+ * when s is. rows = 0 is a no-op.
+ */
+QE_API qe_status qe_mx4_quantize(const void* X, qe_dtype x_dtype, const float* s, int32_t rows, int32_t cols, void* codes,
+                                 void* scales, float* s_inv, void* stream);
+
+/* The values of MXFP4 codes, [rows, cols] in fp32 or bf16 (exact in both); NaN where the scale is NaN. */
+QE_API qe_status qe_mx4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, void* out,
+                                   qe_dtype out_dtype, void* stream);
+
+/*
+ * Y = X . W^T of an MXFP4 X [T, d_in] and an MXFP4 W [d_out, d_in], on the block-scaled 4-bit tensor cores
+ * with fp32 sums, rounded once to y_dtype. Y [T, d_out]. The result is the same from call to call, and a token's row
+ * does not depend on the other tokens' values. A NaN scale makes the whole row (X) or column (W) of Y NaN.
+ * T = 0 is a no-op. T <= 1<<20, d_out <= 1<<24, d_in as above.
+ */
+QE_API qe_status qe_mx4_product(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                                int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype y_dtype, void* stream);
+
+/*
+ * The linear layer on it: quantizes fl32(X * s_inv) (s_inv may be NULL) into the workspace, then
+ * qe_mx4_product. X [T, d_in], fp32 or bf16. workspace (device): at least
+ * qe_mx4_linear_workspace_bytes(T, d_in) bytes; calls that share one must not overlap on the GPU.
+ */
+QE_API size_t qe_mx4_linear_workspace_bytes(int32_t T, int32_t d_in); /* 0 on an invalid shape */
+QE_API qe_status qe_mx4_linear_forward(const void* w_codes, const void* w_scales, const float* s_inv, const void* X,
+                                       qe_dtype x_dtype, int32_t T, int32_t d_in, int32_t d_out, void* Y,
+                                       qe_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Self-test of the bounded device waits (a library convenience; the paper has no counterpart).

@@ -25,7 +25,9 @@ EXPORTS = (
     "qe_last_cuda_error", "qe_device_error", "qe_unpack_weights", "qe_act_quant", "qe_linear_forward_debug",
     "qe_linear_forward_stages", "qe_linear_kernel_launches", "qe_linear_forward_noalloc",
     "qe_selftest_wait_timeout", "qe_split_channels", "qe_cooccurrence_npmi", "qe_pack_adapters_sparse",
-    "qe_linear_plan",
+    "qe_linear_plan", "qe_add_rmsnorm_quant", "qe_act_dequant", "qe_mx4_code_bytes", "qe_mx4_scale_bytes",
+    "qe_mx4_quantize", "qe_mx4_dequantize", "qe_mx4_product", "qe_mx4_linear_workspace_bytes",
+    "qe_mx4_linear_forward", "qe_linear_forward_codes",
 )
 # fixed scratch of qe_linear_forward_noalloc (bytes), as declared in include/qe.h
 NOALLOC_WORKSPACE_BYTES = 32 << 20
@@ -101,6 +103,16 @@ def load() -> ctypes.CDLL:
         "qe_selftest_wait_timeout": ([I, P], I),
         "qe_split_channels": ([P, I, I, I, P, P], I),
         "qe_cooccurrence_npmi": ([P, I, I, P, I, I, P, P, ctypes.c_float, P], I),
+        "qe_linear_forward_codes": ([D, ctypes.POINTER(LayerWeights), P, I, P, P, I, P, I, P, S, P], I),
+        "qe_add_rmsnorm_quant": ([P, I, P, P, I, ctypes.c_double, I, I, P, I, P, P, P, P, P], I),
+        "qe_act_dequant": ([P, P, I, I, P, I, P], I),
+        "qe_mx4_code_bytes": ([I, I], S),
+        "qe_mx4_scale_bytes": ([I, I], S),
+        "qe_mx4_quantize": ([P, I, P, I, I, P, P, P, P], I),
+        "qe_mx4_dequantize": ([P, P, I, I, P, I, P], I),
+        "qe_mx4_product": ([P, P, P, P, I, I, I, P, I, P], I),
+        "qe_mx4_linear_workspace_bytes": ([I, I], S),
+        "qe_mx4_linear_forward": ([P, P, P, P, I, I, I, I, P, I, P, S, P], I),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -224,6 +236,18 @@ def linear_forward(desc, weights: LayerWeights, X, Y, workspace, stream=None):
                                     _stream(stream)), "qe_linear_forward")
 
 
+def linear_forward_codes(desc, weights: LayerWeights, X, codes, sa, Y, workspace, stream=None):
+    """qe_linear_forward for rows that add_rmsnorm_quant or act_quant quantized (codes int8 [T, d_in], sa [T])."""
+    import torch
+    T, K = _rows(X, "X")
+    _expect(X, X.dtype, (T, desc.d_in), "X")
+    _expect(Y, Y.dtype, (T, desc.d_out), "Y")
+    _expect(codes, torch.int8, (T, K), "codes")
+    _expect(sa, torch.float32, (T,), "sa")
+    _launch("qe_linear_forward_codes", stream, ctypes.byref(desc), ctypes.byref(weights), X, _dtype(X), codes, sa, T, Y,
+            _dtype(Y), workspace, workspace.numel() * workspace.element_size())
+
+
 def linear_kernel_launches(desc: LayerDesc, T: int, x_dtype: int = QE_BF16) -> int:
     return int(load().qe_linear_kernel_launches(ctypes.byref(desc), T, x_dtype))
 
@@ -274,6 +298,156 @@ def act_quant(X, s_inv, a_bits, codes, sa, stream=None):
     T, K = X.shape
     _check(load().qe_act_quant(_ptr(X), _dtype(X), _ptr(s_inv), T, K, a_bits, _ptr(codes), _ptr(sa),
                                _stream(stream)), "qe_act_quant")
+
+
+def _launch(what: str, stream, *args):
+    """Calls the entry point on the device of the first tensor among args, with that device's current
+    stream unless one is given. Tensors are passed as their pointers, after a check that all are
+    contiguous CUDA tensors of one device."""
+    import torch
+    dev, raw = None, []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            if not a.is_cuda or not a.is_contiguous():
+                _need_cuda(a)
+            i = a.get_device()
+            if dev is None:
+                dev = i
+            elif i != dev:
+                raise QEError(QE_ERR_INVALID_ARG, "device", f"{what}: tensors on devices {dev} and {i}")
+            raw.append(a.data_ptr())
+        else:
+            raw.append(a)
+    f = getattr(load(), what)
+    if dev is None or dev == torch.cuda.current_device():
+        rc = f(*raw, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*raw, _stream(stream))
+    if rc != QE_OK:
+        _check(rc, what)
+
+
+def _expect(t, dtype, shape, name: str):
+    """Checks a tensor's type and shape (an int: its least number of elements) before its pointer is passed on."""
+    if t.dtype != dtype or (t.numel() < shape if isinstance(shape, int) else tuple(t.shape) != shape):
+        raise QEError(QE_ERR_INVALID_ARG, name, f"expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(t, name: str):
+    if t.dim() != 2:
+        raise QEError(QE_ERR_INVALID_ARG, name, f"expected [rows, channels], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _on(stream):
+    """What is allocated inside belongs to the stream the call runs on (a torch stream or a raw handle),
+    so the allocator never hands it to another stream, or out of a graph's capture, while it is in use."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _scratch(shape, dtype, like):
+    import torch
+    return torch.empty(shape, dtype=dtype or torch.uint8, device=like.device)
+
+
+def add_rmsnorm_quant(X, gamma, eps, a_bits, codes=None, scales=None, residual=None, residual_out=None, Y=None,
+                      s_inv=None, stream=None):
+    """RMS norm of X + residual, with the normed row in Y and quantized into codes and scales.
+
+    a_bits 8/6: codes int8 [T, d], scales fp32 [T]; 4: MXFP4 codes uint8 [T, d/2] and mx4_scale_bytes(T, d)
+    scale bytes; 16: neither.
+    """
+    import torch
+    T, d = _rows(X, "X")
+    _expect(gamma, gamma.dtype, (d,), "gamma")
+    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (Y, "Y")):
+        if t is not None:
+            _expect(t, X.dtype, (T, d), name)
+    if s_inv is not None:
+        _expect(s_inv, torch.float32, (d,), "s_inv")
+    if a_bits == 4 and codes is not None and scales is not None:
+        _expect(codes, torch.uint8, (T, d // 2), "codes")
+        _expect(scales, torch.uint8, mx4_scale_bytes(T, d), "scales")
+    elif a_bits in (6, 8) and codes is not None and scales is not None:
+        _expect(codes, torch.int8, (T, d), "codes")
+        _expect(scales, torch.float32, (T,), "scales")
+    _launch("qe_add_rmsnorm_quant", stream, X, _dtype(X), residual, gamma, _dtype(gamma), float(eps), T, d, s_inv,
+            a_bits, residual_out, Y, codes, scales)
+
+
+def act_dequant(codes, sa, out, stream=None):
+    """out = codes * sa per token (fp32 or bf16)."""
+    import torch
+    T, d = _rows(codes, "codes")
+    _expect(codes, torch.int8, (T, d), "codes")
+    _expect(sa, torch.float32, (T,), "sa")
+    _expect(out, out.dtype, (T, d), "out")
+    _launch("qe_act_dequant", stream, codes, sa, T, d, out, _dtype(out))
+
+
+def mx4_code_bytes(rows: int, cols: int) -> int:
+    return int(load().qe_mx4_code_bytes(rows, cols))
+
+
+def mx4_scale_bytes(rows: int, cols: int) -> int:
+    return int(load().qe_mx4_scale_bytes(rows, cols))
+
+
+def mx4_quantize(X, codes, scales, s=None, s_inv=None, stream=None):
+    """MXFP4 of fl32(X * s): codes uint8 [rows, cols/2], scales uint8 [mx4_scale_bytes(rows, cols)].
+    s_inv (fp32 [cols], with s) receives fl32(1/s)."""
+    import torch
+    rows, cols = _rows(X, "X")
+    _expect(codes, torch.uint8, (rows, cols // 2), "codes")
+    _expect(scales, torch.uint8, mx4_scale_bytes(rows, cols), "scales")
+    for t, name in ((s, "s"), (s_inv, "s_inv")):
+        if t is not None:
+            _expect(t, torch.float32, (cols,), name)
+    _launch("qe_mx4_quantize", stream, X, _dtype(X), s, rows, cols, codes, scales, s_inv)
+
+
+def mx4_dequantize(codes, scales, out, stream=None):
+    """The values of MXFP4 codes, in out's type (fp32 or bf16)."""
+    import torch
+    rows, cols = _rows(out, "out")
+    _expect(codes, torch.uint8, (rows, cols // 2), "codes")
+    _expect(scales, torch.uint8, mx4_scale_bytes(rows, cols), "scales")
+    _launch("qe_mx4_dequantize", stream, codes, scales, rows, cols, out, _dtype(out))
+
+
+def mx4_product(x_codes, x_scales, w_codes, w_scales, Y, stream=None):
+    """Y [T, d_out] = X . W^T of two MXFP4 matrices."""
+    import torch
+    T, N = _rows(Y, "Y")
+    K = 2 * _rows(w_codes, "w_codes")[1]
+    _expect(x_codes, torch.uint8, (T, K // 2), "x_codes")
+    _expect(w_codes, torch.uint8, (N, K // 2), "w_codes")
+    _expect(x_scales, torch.uint8, mx4_scale_bytes(T, K), "x_scales")
+    _expect(w_scales, torch.uint8, mx4_scale_bytes(N, K), "w_scales")
+    _launch("qe_mx4_product", stream, x_codes, x_scales, w_codes, w_scales, T, K, N, Y, _dtype(Y))
+
+
+def mx4_linear_workspace_bytes(T: int, d_in: int) -> int:
+    return int(load().qe_mx4_linear_workspace_bytes(T, d_in))
+
+
+def mx4_linear_forward(w_codes, w_scales, X, Y, workspace, s_inv=None, stream=None):
+    """Y = MXFP4(X * s_inv) . W^T for an MXFP4 W."""
+    import torch
+    T, K = _rows(X, "X")
+    N = _rows(Y, "Y")[1]
+    _expect(Y, Y.dtype, (T, N), "Y")
+    _expect(w_codes, torch.uint8, (N, K // 2), "w_codes")
+    _expect(w_scales, torch.uint8, mx4_scale_bytes(N, K), "w_scales")
+    if s_inv is not None:
+        _expect(s_inv, torch.float32, (K,), "s_inv")
+    _launch("qe_mx4_linear_forward", stream, w_codes, w_scales, s_inv, X, _dtype(X), T, K, N, Y, _dtype(Y), workspace,
+            workspace.numel() * workspace.element_size())
 
 
 def device_error(clear: bool = True, stream=None) -> int:
@@ -348,4 +522,54 @@ class QELayer:
         if Y is None:
             Y = torch.empty((T, self.desc.d_out), dtype=out_dtype or X.dtype, device=X.device)
         linear_forward(self.desc, self.weights, X, Y, self.workspace(T), stream)
+        return Y
+
+    def forward_codes(self, X, codes, sa, out_dtype=None, Y=None, stream=None):
+        """forward for rows that are already quantized (add_rmsnorm_quant with this layer's s_inv and a_bits)."""
+        T = X.shape[0]
+        with _on(stream):
+            Y = _scratch((T, self.desc.d_out), out_dtype or X.dtype, X) if Y is None else Y
+            ws = _scratch((max(256, linear_workspace_bytes(self.desc, T)),), None, X)
+            linear_forward_codes(self.desc, self.weights, X, codes, sa, Y, ws, stream)
+        return Y
+
+
+class Mx4Layer:
+    """One linear layer with its weights in MXFP4, resident on the GPU.
+
+    Built from full-precision weights with `from_float`. `forward` quantizes its input (times s_inv) and
+    multiplies; `forward_codes` takes the MXFP4 activations that add_rmsnorm_quant or mx4_quantize wrote.
+    """
+
+    def __init__(self, w_codes, w_scales, s_inv=None):
+        self.w_codes, self.w_scales, self.s_inv = w_codes, w_scales, s_inv
+        self.d_out, self.d_in = w_codes.shape[0], 2 * w_codes.shape[1]
+
+    @classmethod
+    def from_float(cls, W, s=None, stream=None) -> "Mx4Layer":
+        """W [d_out, d_in] (fp32/bf16); s (fp32 [d_in]): the smoothing factors W is multiplied by, and the
+        input by their reciprocals."""
+        import torch
+        N, K = _rows(W, "W")
+        with _on(stream):
+            codes = _scratch((N, K // 2), None, W)
+            scales = _scratch((mx4_scale_bytes(N, K),), None, W)
+            s_inv = None if s is None else _scratch((K,), torch.float32, W)
+            mx4_quantize(W, codes, scales, s, s_inv, stream)
+        return cls(codes, scales, s_inv)
+
+    def forward(self, X, out_dtype=None, Y=None, stream=None):
+        T = _rows(X, "X")[0]
+        with _on(stream):
+            Y = _scratch((T, self.d_out), out_dtype or X.dtype, X) if Y is None else Y
+            ws = _scratch((mx4_linear_workspace_bytes(T, self.d_in),), None, X)
+            mx4_linear_forward(self.w_codes, self.w_scales, X, Y, ws, self.s_inv, stream)
+        return Y
+
+    def forward_codes(self, codes, scales, out_dtype=None, Y=None, stream=None):
+        import torch
+        with _on(stream):
+            if Y is None:
+                Y = _scratch((_rows(codes, "codes")[0], self.d_out), out_dtype or torch.bfloat16, codes)
+            mx4_product(codes, scales, self.w_codes, self.w_scales, Y, stream)
         return Y

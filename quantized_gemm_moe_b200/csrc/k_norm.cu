@@ -1,0 +1,242 @@
+// The residual's addition and the root-mean-square norm in front of a quantized projection, with the
+// normed row quantized in the same pass, and the dequantization of per-token int8 codes.
+#include <algorithm>
+
+#include "qe_internal.h"
+#include "qe_ptx.cuh"
+#include "qe_quant.cuh"
+
+namespace qe {
+namespace {
+
+struct NormArgs {
+  const void* X;
+  const void* R;       // residual, or nullptr
+  const void* gamma;
+  const float* s_inv;  // or nullptr
+  double eps;
+  int d, qmax, g_bf16;
+  void* H;             // x + r in x's type, or nullptr
+  void* Y;             // normed row in x's type, or nullptr
+  uint8_t* codes;
+  void* scales;        // sa fp32 [T] (int8 codes) or MXFP4 scale tiles
+};
+
+enum { kOutNone = 0, kOutInt8 = 1, kOutMx4 = 2 };
+
+// Eight elements at p + i (16-byte aligned) in fp32.
+__device__ __forceinline__ void ld8(const void* p, size_t i, bool bf16, float (&v)[8]) {
+  if (bf16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
+      v[2 * j + 1] = bf16_bits_to_f32(w[j] >> 16);
+    }
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void st8(void* p, size_t i, bool bf16, const float (&v)[8]) {
+  if (bf16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * j])) |
+             (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * j + 1])) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// One CTA per row. A thread holds VPT vectors of eight neighbouring channels, blockDim.x vectors apart,
+// in registers from the only read of the row to the last write.
+//   h = fl32(x + r); rstd = fl32(1/sqrt(sum h^2 / d + eps)); y = fl32(fl32(h*rstd)*g); v = fl32(y*s_inv)
+// The sum of squares is held in 64 bits and rstd rounded once, after which every value that decides a
+// code is one fp32 operation, so the codes do not depend on the order of the sum.
+template <bool BF16, int VPT, int MAXT, int OUT>
+__global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const NormArgs a) {
+  __shared__ double sum_s[32];
+  __shared__ uint32_t top_s[32];
+  __shared__ float rstd_s;
+  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const size_t row = blockIdx.x, base = row * a.d;
+  float h[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int k = (tid + j * nt) * 8;
+    if (k < a.d) {
+      ld8(a.X, base + k, BF16, h[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
+    }
+  }
+  if (a.R) {
+    float r[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      if (k < a.d) ld8(a.R, base + k, BF16, r[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      if (k < a.d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], r[j][i]);
+        if (a.H) st8(a.H, base + k, BF16, h[j]);
+      }
+    }
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[j][i]), static_cast<double>(h[j][i]), sum);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = lane < nw ? sum_s[lane] : 0.0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) rstd_s = static_cast<float>(1.0 / sqrt(sum / a.d + a.eps));
+  }
+  __syncthreads();
+  const float rstd = rstd_s;
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int k = (tid + j * nt) * 8;
+    if (k < a.d) {
+      float g[8];
+      ld8(a.gamma, k, a.g_bf16, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(__fmul_rn(h[j][i], rstd), g[i]);
+      if (a.Y) st8(a.Y, base + k, BF16, h[j]);
+      if (OUT != kOutNone && a.s_inv) {
+        float s[8];
+        ld8(a.s_inv, k, false, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(h[j][i], s[i]);
+      }
+      if (OUT == kOutInt8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[j][i]) & 0x7FFFFFFFu);
+      }
+    }
+  }
+  if (OUT == kOutInt8) {
+    // magnitudes order as unsigned bit patterns, with infinities and NaNs above every finite value
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) top_s[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, lane < nw ? top_s[lane] : 0u);
+    const bool finite = top < 0x7F800000u;
+    const float sa = finite ? __fdiv_rn(__uint_as_float(top), static_cast<float>(a.qmax)) : __uint_as_float(0x7FC00000u);
+    if (tid == 0) static_cast<float*>(a.scales)[row] = sa;
+    const float inv = sa > 0.0f ? __frcp_rn(sa) : 0.0f;
+    const bool fast = rtn_fast_ok(sa, inv);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      if (k < a.d) {
+        uint32_t w0 = 0, w1 = 0;
+        if (finite) rtn_code8(h[j], sa, inv, fast, a.qmax, w0, w1);
+        *reinterpret_cast<uint2*>(a.codes + base + k) = make_uint2(w0, w1);
+      }
+    }
+  }
+  if (OUT == kOutMx4) {
+    const size_t KT = (a.d + kMxTileCols - 1) / kMxTileCols;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      uint32_t word;
+      const uint32_t c = mx_quantize8(h[j], k < a.d, lane, word);
+      if (k < a.d) {
+        *reinterpret_cast<uint32_t*>(a.codes + (base + k) / 2) = c;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + mx_scale_word(row, k / kMxTileCols, KT)) = word;
+      }
+    }
+  }
+}
+
+// out[t][k] = codes[t][k] * sa[t], eight channels per thread.
+__global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ codes, const float* __restrict__ sa,
+                                                     int d8, size_t n8, void* __restrict__ out, int out_bf16) {
+  const size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x;
+  if (i >= n8) return;
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+  const float s = __ldg(sa + i / d8);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = static_cast<float>(static_cast<int8_t>(w.x >> (8 * j))) * s;
+    v[4 + j] = static_cast<float>(static_cast<int8_t>(w.y >> (8 * j))) * s;
+  }
+  st8(out, i * 8, out_bf16, v);
+}
+
+template <bool BF16, int VPT, int MAXT>
+cudaError_t launch_norm_t(const NormArgs& a, int out, int T, cudaStream_t st) {
+  const int threads = static_cast<int>(round_up(ceil_div(a.d / 8, VPT), 32));
+  if (threads > MAXT) return cudaErrorInvalidConfiguration;
+  if (out == kOutInt8) k_add_rmsnorm<BF16, VPT, MAXT, kOutInt8><<<T, threads, 0, st>>>(a);
+  else if (out == kOutMx4) k_add_rmsnorm<BF16, VPT, MAXT, kOutMx4><<<T, threads, 0, st>>>(a);
+  else k_add_rmsnorm<BF16, VPT, MAXT, kOutNone><<<T, threads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_norm_x(const NormArgs& a, int out, int T, cudaStream_t st) {
+  const int vecs = a.d / 8;
+  if (vecs <= 256) return launch_norm_t<BF16, 1, 1024>(a, out, T, st);
+  if (vecs <= 512) return launch_norm_t<BF16, 2, 1024>(a, out, T, st);
+  if (vecs <= 1024) return launch_norm_t<BF16, 4, 256>(a, out, T, st);
+  return launch_norm_t<BF16, 4, 1024>(a, out, T, st);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const void* gamma, bool g_bf16, double eps,
+                               int T, int d, const float* s_inv, int a_bits, void* H, void* Y, void* codes,
+                               void* scales, cudaStream_t st) {
+  if (T == 0) return cudaSuccess;
+  NormArgs a{};
+  a.X = X;
+  a.R = R;
+  a.gamma = gamma;
+  a.s_inv = s_inv;
+  a.eps = eps;
+  a.d = d;
+  a.qmax = (1 << (a_bits - 1)) - 1;
+  a.g_bf16 = g_bf16;
+  a.H = H;
+  a.Y = Y;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  const int out = a_bits == 16 ? kOutNone : a_bits == 4 ? kOutMx4 : kOutInt8;
+  return x_bf16 ? launch_norm_x<true>(a, out, T, st) : launch_norm_x<false>(a, out, T, st);
+}
+
+cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int d, void* out, bool out_bf16,
+                               cudaStream_t st) {
+  const size_t n8 = static_cast<size_t>(T) * (d / 8);
+  if (n8 == 0) return cudaSuccess;
+  k_act_dequant<<<static_cast<unsigned>(ceil_div(n8, 256)), 256, 0, st>>>(codes, sa, d / 8, n8, out, out_bf16);
+  return cudaGetLastError();
+}
+
+}  // namespace qe

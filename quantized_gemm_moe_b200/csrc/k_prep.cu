@@ -8,6 +8,7 @@
 
 #include "qe_internal.h"
 #include "qe_ptx.cuh"
+#include "qe_quant.cuh"
 
 namespace qe {
 
@@ -64,12 +65,6 @@ cudaError_t read_device_error(int* value, bool clear, cudaStream_t st) {
 
 namespace {
 
-__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
-__device__ __forceinline__ uint16_t f32_to_bf16_bits(float v) {
-  __nv_bfloat16 h = __float2bfloat16_rn(v);
-  return *reinterpret_cast<uint16_t*>(&h);
-}
-
 // Loads 8 consecutive elements x[row][k0..k0+8) as fp32 (k0 multiple of 8, row pitch K).
 template <bool BF16>
 __device__ __forceinline__ void load8(const void* X, size_t row, int K, int k0, float (&v)[8]) {
@@ -94,64 +89,6 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-// One symmetric RTN code: clamp(rint(fl32(v / scale)), -qmax, qmax); zero scale -> 0.
-__device__ __forceinline__ int rtn_code(float v, float scale, int qmax) {
-  if (scale == 0.0f) return 0;
-  float r = rintf(__fdiv_rn(v, scale));
-  r = fminf(fmaxf(r, -static_cast<float>(qmax)), static_cast<float>(qmax));
-  return static_cast<int>(r);
-}
-
-// Eight codes through rtn_code, packed little-endian into two words. Kept out of line: callers
-// unroll their loops, and this rare path would otherwise be copied into every unrolled step.
-__device__ __noinline__ uint2 rtn_code8_exact(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
-                                              float v7, float scale, int qmax) {
-  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
-  uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w0 |= (static_cast<uint32_t>(rtn_code(v[i], scale, qmax)) & 0xFFu) << (8 * i);
-    w1 |= (static_cast<uint32_t>(rtn_code(v[4 + i], scale, qmax)) & 0xFFu) << (8 * i);
-  }
-  return make_uint2(w0, w1);
-}
-
-// Eight codes rtn_code(v[i], scale, qmax), packed little-endian into two words, without a division
-// in the common case. inv = fl32(1/scale), the correctly rounded reciprocal. g = fl32(v*inv) differs
-// from the correctly rounded quotient fl32(v/scale) by at most 3 units of 2^-24 |g|, so rint(g)
-// equals rint(fl32(v/scale)) unless g lies within that distance of a half-integer; the test below
-// asks for a margin of 2^-20 |g| and sends the rest through rtn_code. The fast path also needs a
-// normal scale, and |g| < qmax + 0.5 so that the clamp does not bind (|v| <= absmax keeps
-// |g| <= qmax (1 + 2^-22) when the scale came from this row's absmax).
-// rint uses the 1.5*2^23 trick: fl32(g + 1.5*2^23) holds rint(g) (half to even) in its low bits.
-__device__ __forceinline__ void rtn_code8(const float (&v)[8], float scale, float inv, bool fast, int qmax,
-                                          uint32_t& w0, uint32_t& w1) {
-  constexpr float kM = 12582912.0f;
-  const float qmax_f = static_cast<float>(qmax) + 0.5f;
-  uint32_t b[8];
-  bool ok = fast;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float g = __fmul_rn(v[i], inv);
-    const float t = __fadd_rn(g, kM);
-    const float d = fabsf(__fsub_rn(g, __fsub_rn(t, kM)));
-    ok = ok && (__fmaf_rn(fabsf(g), 9.5367431640625e-07f, d) < 0.5f) && (fabsf(g) < qmax_f);
-    b[i] = __float_as_uint(t);
-  }
-  if (ok) {
-    w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-    return;
-  }
-  const uint2 w = rtn_code8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], scale, qmax);
-  w0 = w.x;
-  w1 = w.y;
-}
-// Whether rtn_code8's fast path may be used for this scale (and its reciprocal).
-__device__ __forceinline__ bool rtn_fast_ok(float scale, float inv) {
-  return scale >= 1.17549435e-38f && inv < 3.0e38f;
 }
 
 // ------------------------------------------------------------------ router + absmax
@@ -651,6 +588,8 @@ __device__ bool grid_barrier(unsigned* ctr, int* err) {
 //  quant:  at row p = pos[t]: the activation codes (or bf16(x*s_inv) for weight-only layers),
 //          sa_sorted[p], and U_cat[p] = fp16((sum of U slots, routed columns of the other experts
 //          zeroed) / su[p]), su[p] a power of two that puts the row's largest |U| in [2^13, 2^14).
+// PRE: the rows were quantized by an earlier operator; quant copies their codes (pre_codes, token order)
+// and scales (pre_sa) to the bucket positions, and neither step reads X for them.
 struct RouteQuantArgs {
   const float* partial;
   int nslots, R_tot, R_pad, R_rt, n_r, r_s, r_r, R_a;
@@ -676,6 +615,8 @@ struct RouteQuantArgs {
   float* su_sorted;
   unsigned* zero_words;
   int n_zero_words;
+  const int8_t* pre_codes;
+  const float* pre_sa;
   int* err;
 };
 
@@ -737,7 +678,7 @@ size_t route_quant_smem(int K, int chunk, int R_pad) {
   return size_t(K) * 4 + size_t(kRQThreads / 32) * R_pad * 4 + size_t(chunk) * 12;
 }
 
-template <bool BF16>
+template <bool BF16, bool PRE>
 __global__ void __launch_bounds__(kRQThreads) k_route_quant(const RouteQuantArgs a) {
   constexpr int kWarps = kRQThreads / 32;
   constexpr int kB = RowBatch<BF16>::kIters;
@@ -808,7 +749,7 @@ __global__ void __launch_bounds__(kRQThreads) k_route_quant(const RouteQuantArgs
           e_s[t - t0] = bi;
         }
       }
-      if (a.sa_tok && BF16) {
+      if (a.sa_tok && BF16 && !PRE) {
         float mx = 0.0f;
         for (int k0 = (sub * 32 + lane) * 8; k0 < a.K; k0 += 256 * wpt * kB) {
           RowRaw<true> r;
@@ -838,8 +779,13 @@ __global__ void __launch_bounds__(kRQThreads) k_route_quant(const RouteQuantArgs
     __syncthreads();
     if (a.sa_tok) {
       for (int i = threadIdx.x; i < t1 - t0; i += kRQThreads) {
-        const float mx = BF16 ? __int_as_float(mx_s[i]) : a.amax[t0 + i];
-        const float sa = __fdiv_rn(mx, static_cast<float>(a.qmax));
+        float sa;
+        if constexpr (PRE) {
+          sa = a.pre_sa[t0 + i];
+        } else {
+          const float mx = BF16 ? __int_as_float(mx_s[i]) : a.amax[t0 + i];
+          sa = __fdiv_rn(mx, static_cast<float>(a.qmax));
+        }
         a.sa_tok[t0 + i] = sa;
         mx_s[i] = __float_as_int(sa);  // the quantization below reads it from here
       }
@@ -931,7 +877,21 @@ __global__ void __launch_bounds__(kRQThreads) k_route_quant(const RouteQuantArgs
     const float sa = a.codes ? (a.do_route ? __int_as_float(mx_s[t - t0]) : a.sa_tok[t]) : 0.0f;
     const float inv = (sa > 0.0f) ? __frcp_rn(sa) : 0.0f;
     const bool fast = rtn_fast_ok(sa, inv);
-    for (int k0 = (sub * 32 + lane) * 8; k0 < a.K; k0 += 256 * wpt * kB) {
+    if constexpr (PRE) {
+      // K is a multiple of 16: the group is 64 or 128
+      const uint4* src = reinterpret_cast<const uint4*>(a.pre_codes + static_cast<size_t>(t) * a.K);
+      uint4* dst = reinterpret_cast<uint4*>(a.codes + p * a.K);
+      for (int i0 = sub * 32 + lane; i0 < a.K / 16; i0 += 32 * wpt * 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + 32 * wpt * j < a.K / 16) w[j] = __ldg(src + i0 + 32 * wpt * j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + 32 * wpt * j < a.K / 16) dst[i0 + 32 * wpt * j] = w[j];
+      }
+    }
+    for (int k0 = (sub * 32 + lane) * 8; !PRE && k0 < a.K; k0 += 256 * wpt * kB) {
       RowRaw<BF16> r;
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
@@ -1190,12 +1150,16 @@ int route_quant_grid() {
     int dev = 0, sms = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return 0;
-    if (cudaFuncSetAttribute(k_route_quant<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
+    if (cudaFuncSetAttribute(k_route_quant<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(k_route_quant<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
+        cudaFuncSetAttribute(k_route_quant<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(k_route_quant<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(k_route_quant<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRQMaxSmem) !=
             cudaSuccess)
       return 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_route_quant<true>, kRQThreads, kRQMaxSmem) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_route_quant<true, false>, kRQThreads, kRQMaxSmem) !=
             cudaSuccess ||
         per_sm < 1)
       return 0;
@@ -1258,8 +1222,13 @@ cudaError_t launch_route_quant(const RouteQuantParams& q, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (q.x_bf16) return cudaLaunchKernelEx(&cfg, k_route_quant<true>, a);
-  return cudaLaunchKernelEx(&cfg, k_route_quant<false>, a);
+  a.pre_codes = q.pre_codes;
+  a.pre_sa = q.pre_sa;
+  if (q.pre_codes)
+    return q.x_bf16 ? cudaLaunchKernelEx(&cfg, k_route_quant<true, true>, a)
+                    : cudaLaunchKernelEx(&cfg, k_route_quant<false, true>, a);
+  if (q.x_bf16) return cudaLaunchKernelEx(&cfg, k_route_quant<true, false>, a);
+  return cudaLaunchKernelEx(&cfg, k_route_quant<false, false>, a);
 }
 
 cudaError_t launch_splitk_reduce(const float* partial, int splits, const int32_t* perm, int T, int N, void* Y,

@@ -190,7 +190,8 @@ qe_status check_forward_args(const qe_layer_desc* d, const qe_layer_weights* w, 
 
 qe_status forward_impl(const qe_layer_desc* d, const qe_layer_weights* w, const void* X, qe_dtype xd, int32_t T,
                        void* Y, qe_dtype yd, void* ws, size_t ws_bytes, int32_t* dbg_acc, int32_t* dbg_expert,
-                       int32_t* dbg_perm, float* dbg_sa, int32_t stages, cudaStream_t st) {
+                       int32_t* dbg_perm, float* dbg_sa, int32_t stages, cudaStream_t st,
+                       const int8_t* pre_codes = nullptr, const float* pre_sa = nullptr) {
   qe_status s = check_forward_args(d, w, X, xd, T, Y, yd);
   if (s != QE_OK || T == 0) return s;
   const bool x_bf16 = xd == QE_BF16;
@@ -286,6 +287,8 @@ qe_status forward_impl(const qe_layer_desc* d, const qe_layer_weights* w, const 
     q.su_sorted = su_sorted;
     q.zero_words = p.dec ? at<unsigned>(ws, p.off_dcnt) : nullptr;
     q.n_zero_words = p.dec ? p.dp.cnt_words : 0;
+    q.pre_codes = pre_codes;
+    q.pre_sa = pre_sa;
     q.err = err;
     QE_CUDA(launch_route_quant(q, st), "route_quant");
   }
@@ -344,6 +347,49 @@ qe_status forward_impl(const qe_layer_desc* d, const qe_layer_weights* w, const 
   if (dbg_expert) QE_CUDA(cudaMemcpyAsync(dbg_expert, expert, size_t(T) * 4, cudaMemcpyDeviceToDevice, st), "copy");
   if (dbg_perm) QE_CUDA(cudaMemcpyAsync(dbg_perm, perm, size_t(T) * 4, cudaMemcpyDeviceToDevice, st), "copy");
   if (dbg_sa) QE_CUDA(cudaMemcpyAsync(dbg_sa, sa_tok, size_t(T) * 4, cudaMemcpyDeviceToDevice, st), "copy");
+  return QE_OK;
+}
+
+// ------------------------------------------------------------------ MXFP4
+// Scale bytes of a [rows, cols] matrix: tiles of 128 rows x 128 channels.
+size_t mx4_scale_bytes(int64_t rows, int64_t cols) { return size_t(ceil_div(rows, 128)) * size_t(ceil_div(cols, 128)) * 512; }
+// rows <= 1<<24; cols a multiple of the block, <= 1<<20
+qe_status check_mx4_shape(int32_t rows, int32_t cols) {
+  if (rows < 0 || cols <= 0) return QE_ERR_INVALID_ARG;
+  if (cols % 32 != 0) return QE_ERR_INVALID_ARG;
+  if (rows > (1 << 24) || cols > (1 << 20)) return QE_ERR_UNSUPPORTED;
+  return QE_OK;
+}
+bool is_dtype(qe_dtype t) { return t == QE_F32 || t == QE_BF16; }
+
+struct Mx4Workspace {
+  size_t off_scales, bytes;
+};
+Mx4Workspace mx4_workspace(int32_t T, int32_t d_in) {
+  Mx4Workspace w;
+  w.off_scales = align256(size_t(T) * (d_in / 2));
+  w.bytes = w.off_scales + align256(mx4_scale_bytes(T, d_in));
+  return w;
+}
+
+qe_status check_mx4_product(int32_t T, int32_t d_in, int32_t d_out, qe_dtype yd) {
+  qe_status s = check_mx4_shape(d_out, d_in);
+  if (s != QE_OK) return s;
+  if (T < 0 || T > (1 << 20) || d_out < 1 || !is_dtype(yd)) return QE_ERR_INVALID_ARG;
+  return QE_OK;
+}
+
+// Both operands quantized; T > 0 and everything checked.
+qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                           int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype yd, cudaStream_t st) {
+  const Mx4Plan p = plan_mx4(T, d_out, d_in);
+  CUtensorMap tm_w, tm_x;
+  qe_status s;
+  if ((s = make_tmap(&tm_w, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, d_out, 128, 128)) != QE_OK) return s;
+  if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128, p.bn)) != QE_OK) return s;
+  QE_CUDA(launch_mx4_product(tm_w, tm_x, p, static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(x_scales),
+                             T, d_out, d_in, Y, yd == QE_BF16, device_error_ptr(), st),
+          "mx4_product");
   return QE_OK;
 }
 
@@ -489,6 +535,19 @@ qe_status qe_linear_forward(const qe_layer_desc* desc, const qe_layer_weights* w
                       nullptr, nullptr, QE_STAGE_ALL, static_cast<cudaStream_t>(stream));
 }
 
+qe_status qe_linear_forward_codes(const qe_layer_desc* desc, const qe_layer_weights* weights, const void* X,
+                                  qe_dtype x_dtype, const int8_t* codes, const float* sa, int32_t T, void* Y,
+                                  qe_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const qe_status s = check_forward_args(desc, weights, X, x_dtype, T, Y, y_dtype);
+  if (s != QE_OK) return s;
+  if (desc->a_bits == 16) return QE_ERR_UNSUPPORTED;
+  if (T == 0) return QE_OK;
+  if (!codes || !sa) return QE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(sa)) return QE_ERR_ALIGNMENT;
+  return forward_impl(desc, weights, X, x_dtype, T, Y, y_dtype, workspace, workspace_bytes, nullptr, nullptr, nullptr,
+                      nullptr, QE_STAGE_ALL, static_cast<cudaStream_t>(stream), codes, sa);
+}
+
 int32_t qe_linear_kernel_launches(const qe_layer_desc* desc, int32_t T, qe_dtype x_dtype) {
   if (check_desc(desc) != QE_OK || T < 0) return -1;
   if (T == 0) return 0;
@@ -603,6 +662,117 @@ qe_status qe_device_error(void* stream, int32_t* code, int32_t clear) {
   QE_CUDA(read_device_error(&v, clear != 0, static_cast<cudaStream_t>(stream)), "device_error");
   if (code) *code = v;
   return v ? QE_ERR_TIMEOUT : QE_OK;
+}
+
+qe_status qe_add_rmsnorm_quant(const void* X, qe_dtype x_dtype, const void* residual, const void* gamma,
+                               qe_dtype gamma_dtype, double eps, int32_t T, int32_t d, const float* s_inv,
+                               int32_t a_bits, void* residual_out, void* Y, void* codes, void* scales, void* stream) {
+  if (T < 0 || T > (1 << 20) || d <= 0) return QE_ERR_INVALID_ARG;
+  if (a_bits != 4 && a_bits != 6 && a_bits != 8 && a_bits != 16) return QE_ERR_UNSUPPORTED;
+  if (d % (a_bits == 4 ? 32 : 8) != 0 || d > kMaxNormD) return QE_ERR_UNSUPPORTED;
+  if (!is_dtype(x_dtype) || !is_dtype(gamma_dtype)) return QE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0) || eps > 3.0e38) return QE_ERR_INVALID_ARG;
+  if (residual_out && !residual) return QE_ERR_INVALID_ARG;
+  if (!gamma) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (a_bits == 16 && !Y && !residual_out) return QE_ERR_INVALID_ARG;
+  if (!X || (a_bits != 16 && (!codes || !scales))) return QE_ERR_INVALID_ARG;
+  for (const void* p : {X, residual, gamma, static_cast<const void*>(s_inv), static_cast<const void*>(residual_out),
+                        static_cast<const void*>(Y), static_cast<const void*>(codes), static_cast<const void*>(scales)})
+    if (!aligned16(p)) return QE_ERR_ALIGNMENT;
+  QE_CUDA(launch_add_rmsnorm(X, x_dtype == QE_BF16, residual, gamma, gamma_dtype == QE_BF16, eps, T, d, s_inv, a_bits,
+                             residual_out, Y, codes, scales, static_cast<cudaStream_t>(stream)),
+          "add_rmsnorm_quant");
+  return QE_OK;
+}
+
+qe_status qe_act_dequant(const int8_t* codes, const float* sa, int32_t T, int32_t d_in, void* out, qe_dtype out_dtype,
+                         void* stream) {
+  if (T < 0 || T > (1 << 20) || d_in <= 0) return QE_ERR_INVALID_ARG;
+  if (d_in % 8 != 0 || d_in > (1 << 20)) return QE_ERR_UNSUPPORTED;
+  if (!is_dtype(out_dtype)) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (!codes || !sa || !out) return QE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(sa) || !aligned16(out)) return QE_ERR_ALIGNMENT;
+  QE_CUDA(launch_act_dequant(codes, sa, T, d_in, out, out_dtype == QE_BF16, static_cast<cudaStream_t>(stream)),
+          "act_dequant");
+  return QE_OK;
+}
+
+size_t qe_mx4_code_bytes(int32_t rows, int32_t cols) {
+  return check_mx4_shape(rows, cols) == QE_OK ? size_t(rows) * size_t(cols / 2) : 0;
+}
+
+size_t qe_mx4_scale_bytes(int32_t rows, int32_t cols) {
+  return check_mx4_shape(rows, cols) == QE_OK ? mx4_scale_bytes(rows, cols) : 0;
+}
+
+qe_status qe_mx4_quantize(const void* X, qe_dtype x_dtype, const float* s, int32_t rows, int32_t cols, void* codes,
+                          void* scales, float* s_inv, void* stream) {
+  const qe_status st = check_mx4_shape(rows, cols);
+  if (st != QE_OK) return st;
+  if (!is_dtype(x_dtype) || (s_inv && !s)) return QE_ERR_INVALID_ARG;
+  if (rows == 0) return QE_OK;
+  if (!X || !codes || !scales) return QE_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(s) || !aligned16(codes) || !aligned16(scales) || !aligned16(s_inv))
+    return QE_ERR_ALIGNMENT;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  QE_CUDA(launch_mx4_quantize(X, x_dtype == QE_BF16, s, rows, cols, static_cast<uint8_t*>(codes),
+                              static_cast<uint8_t*>(scales), cs),
+          "mx4_quantize");
+  if (s_inv) QE_CUDA(launch_recip(s, cols, s_inv, cs), "recip");
+  return QE_OK;
+}
+
+qe_status qe_mx4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, void* out,
+                            qe_dtype out_dtype, void* stream) {
+  const qe_status st = check_mx4_shape(rows, cols);
+  if (st != QE_OK) return st;
+  if (!is_dtype(out_dtype)) return QE_ERR_INVALID_ARG;
+  if (rows == 0) return QE_OK;
+  if (!codes || !scales || !out) return QE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return QE_ERR_ALIGNMENT;
+  QE_CUDA(launch_mx4_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, cols, out,
+                                out_dtype == QE_BF16, static_cast<cudaStream_t>(stream)),
+          "mx4_dequantize");
+  return QE_OK;
+}
+
+qe_status qe_mx4_product(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                         int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype y_dtype, void* stream) {
+  const qe_status st = check_mx4_product(T, d_in, d_out, y_dtype);
+  if (st != QE_OK) return st;
+  if (!w_codes || !w_scales) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (!x_codes || !x_scales || !Y) return QE_ERR_INVALID_ARG;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
+    return QE_ERR_ALIGNMENT;
+  return mx4_product_impl(x_codes, x_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t qe_mx4_linear_workspace_bytes(int32_t T, int32_t d_in) {
+  if (check_mx4_shape(0, d_in) != QE_OK || T < 0 || T > (1 << 20)) return 0;
+  return mx4_workspace(T, d_in).bytes;
+}
+
+qe_status qe_mx4_linear_forward(const void* w_codes, const void* w_scales, const float* s_inv, const void* X,
+                                qe_dtype x_dtype, int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype y_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  qe_status st = check_mx4_product(T, d_in, d_out, y_dtype);
+  if (st != QE_OK) return st;
+  if (!w_codes || !w_scales || !is_dtype(x_dtype)) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (!X || !Y) return QE_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(s_inv))
+    return QE_ERR_ALIGNMENT;
+  const Mx4Workspace w = mx4_workspace(T, d_in);
+  if (!workspace || workspace_bytes < w.bytes) return QE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QE_ERR_ALIGNMENT;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  QE_CUDA(launch_mx4_quantize(X, x_dtype == QE_BF16, s_inv, T, d_in, codes, codes + w.off_scales, cs), "mx4_quantize");
+  return mx4_product_impl(codes, codes + w.off_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype, cs);
 }
 
 qe_status qe_split_channels(const int32_t* hist, int32_t d_in, int32_t k, int32_t C, int32_t* channel_pos,

@@ -153,6 +153,8 @@ struct RouteQuantParams {
   float* su_sorted;
   unsigned* zero_words;  // cleared by the launch (the decode product's tile counters), may be null
   int n_zero_words;
+  const int8_t* pre_codes;  // codes [T][K] and scales [T] of rows quantized before, or null
+  const float* pre_sa;
   int* err;
 };
 cudaError_t launch_route_quant(const RouteQuantParams& q, cudaStream_t st);
@@ -224,6 +226,32 @@ int* device_error_ptr();  // nullptr when the symbol lookup fails
 // caches of device symbol addresses.
 void* current_context();
 cudaError_t read_device_error(int* value, bool clear, cudaStream_t st);
+
+// ------------------------------------------------------------------ norm and MXFP4
+constexpr int kMaxNormD = 32768;  // a row is held in one CTA's registers
+
+// h = x + r, y = h * rstd * gamma, and the quantized fl32(y * s_inv): a_bits 8/6 int8 codes and sa [T],
+// 4 MXFP4 codes and scale tiles, 16 none. R, H, Y and s_inv may be null.
+cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const void* gamma, bool g_bf16, double eps,
+                               int T, int d, const float* s_inv, int a_bits, void* H, void* Y, void* codes,
+                               void* scales, cudaStream_t st);
+cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int d, void* out, bool out_bf16,
+                               cudaStream_t st);
+// s: per-channel factor, or null.
+cudaError_t launch_mx4_quantize(const void* X, bool x_bf16, const float* s, int rows, int cols, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
+                                  bool out_bf16, cudaStream_t st);
+
+// How the MXFP4 product runs: tiles of 128 output channels x bn tokens, K split over clusters of
+// `splits` CTAs. tm_w boxes are 128 rows, tm_x boxes bn rows, both 128 bytes of codes wide.
+struct Mx4Plan {
+  int bn, n_tiles, t_tiles, splits;
+};
+Mx4Plan plan_mx4(int T, int N, int K);
+cudaError_t launch_mx4_product(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
+                               const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, int* err,
+                               cudaStream_t st);
 
 // Top-k importance. bf16 rows with 7680 <= K <= 30720 take the streaming kernel (one CTA per
 // SM, rows staged by bulk copies); others, and rows it leaves unresolved, the radix-select kernel.

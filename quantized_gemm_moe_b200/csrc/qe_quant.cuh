@@ -1,0 +1,142 @@
+// Quantization arithmetic shared by the kernels that write activation codes: bf16 conversion, the
+// symmetric integer codes (A6/A8, W4/W3) and the MXFP4 block (E2M1 codes, E8M0 scale).
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace qe {
+
+__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16_bits(float v) {
+  __nv_bfloat16 h = __float2bfloat16_rn(v);
+  return *reinterpret_cast<uint16_t*>(&h);
+}
+
+// One symmetric RTN code: clamp(rint(fl32(v / scale)), -qmax, qmax); zero scale -> 0.
+__device__ __forceinline__ int rtn_code(float v, float scale, int qmax) {
+  if (scale == 0.0f) return 0;
+  float r = rintf(__fdiv_rn(v, scale));
+  r = fminf(fmaxf(r, -static_cast<float>(qmax)), static_cast<float>(qmax));
+  return static_cast<int>(r);
+}
+
+// Eight codes through rtn_code, packed little-endian into two words. Kept out of line: callers
+// unroll their loops, and this rare path would otherwise be copied into every unrolled step.
+static __device__ __noinline__ uint2 rtn_code8_exact(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
+                                              float v7, float scale, int qmax) {
+  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+  uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w0 |= (static_cast<uint32_t>(rtn_code(v[i], scale, qmax)) & 0xFFu) << (8 * i);
+    w1 |= (static_cast<uint32_t>(rtn_code(v[4 + i], scale, qmax)) & 0xFFu) << (8 * i);
+  }
+  return make_uint2(w0, w1);
+}
+
+// Eight codes rtn_code(v[i], scale, qmax), packed little-endian into two words, without a division
+// in the common case. inv = fl32(1/scale), the correctly rounded reciprocal. g = fl32(v*inv) differs
+// from the correctly rounded quotient fl32(v/scale) by at most 3 units of 2^-24 |g|, so rint(g)
+// equals rint(fl32(v/scale)) unless g lies within that distance of a half-integer; the test below
+// asks for a margin of 2^-20 |g| and sends the rest through rtn_code. The fast path also needs a
+// normal scale, and |g| < qmax + 0.5 so that the clamp does not bind (|v| <= absmax keeps
+// |g| <= qmax (1 + 2^-22) when the scale came from this row's absmax).
+// rint uses the 1.5*2^23 trick: fl32(g + 1.5*2^23) holds rint(g) (half to even) in its low bits.
+__device__ __forceinline__ void rtn_code8(const float (&v)[8], float scale, float inv, bool fast, int qmax,
+                                          uint32_t& w0, uint32_t& w1) {
+  constexpr float kM = 12582912.0f;
+  const float qmax_f = static_cast<float>(qmax) + 0.5f;
+  uint32_t b[8];
+  bool ok = fast;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float g = __fmul_rn(v[i], inv);
+    const float t = __fadd_rn(g, kM);
+    const float d = fabsf(__fsub_rn(g, __fsub_rn(t, kM)));
+    ok = ok && (__fmaf_rn(fabsf(g), 9.5367431640625e-07f, d) < 0.5f) && (fabsf(g) < qmax_f);
+    b[i] = __float_as_uint(t);
+  }
+  if (ok) {
+    w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    return;
+  }
+  const uint2 w = rtn_code8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], scale, qmax);
+  w0 = w.x;
+  w1 = w.y;
+}
+// Whether rtn_code8's fast path may be used for this scale (and its reciprocal).
+__device__ __forceinline__ bool rtn_fast_ok(float scale, float inv) {
+  return scale >= 1.17549435e-38f && inv < 3.0e38f;
+}
+
+// ------------------------------------------------------------------ MXFP4
+// 32 consecutive channels of a row share a scale 2^E, stored as the byte E + 127 (E8M0); the codes are
+// E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6). E = floor(log2 max|v|) - 2
+// puts the largest magnitude into [4, 8), the top binade of E2M1, where it saturates at 6; E is kept in
+// [-127, 127]. A block that holds a NaN or an infinity gets the byte 255 (NaN) and codes 0, so that it
+// stays visible in whatever is computed from it.
+constexpr int kMxBlock = 32;
+constexpr int kMxTileRows = 128;   // rows and
+constexpr int kMxTileCols = 128;   // channels of a tile of scale bytes (512 bytes)
+constexpr int kMxTileBytes = 512;
+constexpr uint32_t kMxOnes = 0x7F7F7F7Fu;  // four scales of one
+
+// Byte offset of the four scales of row r, channels [128*kt, 128*kt + 128); KT = ceil(cols / 128).
+// The order inside a tile is the one tcgen05.cp 32x128b spreads over the tensor memory lanes: 16 bytes
+// for each row r % 32, four for each r / 32.
+__host__ __device__ __forceinline__ size_t mx_scale_word(size_t r, size_t kt, size_t KT) {
+  return ((r >> 7) * KT + kt) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// Scale byte of a block whose largest |v| has the bits `top` (fp32, sign cleared).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return 255u;
+  const int e = static_cast<int>(top >> 23) - 2;  // (field - 127) - 2 + 127; subnormals clamp below
+  return static_cast<uint32_t>(e > 0 ? e : 0);
+}
+// 2^-E for a scale byte below 255 (E in [-127, 125], so the factor is a normal number).
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^E of a scale byte; NaN for 255.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Eight E2M1 codes of a[i], ties to even, saturating at 6; code i in bits [4i, 4i+4).
+__device__ __forceinline__ uint32_t e2m1_pack8(const float (&a)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(a[0]), "f"(a[1]), "f"(a[2]), "f"(a[3]), "f"(a[4]), "f"(a[5]), "f"(a[6]), "f"(a[7]));
+  return w;
+}
+
+// MXFP4 of 8 values per lane: four neighbouring lanes hold a block. Every lane of the warp calls it; a
+// lane past the row's end passes zeros and valid = false. Returns this lane's eight codes; `word`
+// receives the scale bytes of the 16-lane group's four blocks (127, a scale of one, for absent ones).
+// v * 2^-E is exact unless it falls below fp32's normal range, where the code is 0 either way.
+__device__ __forceinline__ uint32_t mx_quantize8(const float (&v)[8], bool valid, int lane, uint32_t& word) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t byte = mx_scale_byte(top);
+  uint32_t w = (valid ? byte : 127u) << (8 * ((lane >> 2) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  w |= __shfl_xor_sync(0xffffffffu, w, 8);
+  word = w;
+  const float inv = mx_inv_scale(byte == 255u ? 127u : byte);
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = v[i] * inv;
+  return byte == 255u ? 0u : e2m1_pack8(a);
+}
+
+}  // namespace qe
