@@ -9,6 +9,7 @@ There is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -301,16 +302,17 @@ def act_quant(X, s_inv, a_bits, codes, sa, stream=None):
 
 
 def _launch(what: str, stream, *args):
-    """Calls the entry point on the device of the first tensor among args, with that device's current
-    stream unless one is given. Tensors are passed as their pointers, after a check that all are
-    contiguous CUDA tensors of one device."""
+    """Calls the entry point on the device of its tensors, with that device's current stream unless one is
+    given. Tensors are passed as their pointers, after a check that all are contiguous CUDA tensors of one
+    device. (The current stream and device come from torch's raw getters: a decoded token's launch takes
+    less time than torch.cuda.current_stream() builds its object in.)"""
     import torch
-    dev, raw = None, []
+    dev, raw, Tensor = None, [], torch.Tensor
     for a in args:
-        if isinstance(a, torch.Tensor):
-            if not a.is_cuda or not a.is_contiguous():
-                _need_cuda(a)
+        if isinstance(a, Tensor):
             i = a.get_device()
+            if i < 0 or not a.is_contiguous():
+                _need_cuda(a)
             if dev is None:
                 dev = i
             elif i != dev:
@@ -318,19 +320,23 @@ def _launch(what: str, stream, *args):
             raw.append(a.data_ptr())
         else:
             raw.append(a)
-    f = getattr(load(), what)
-    if dev is None or dev == torch.cuda.current_device():
-        rc = f(*raw, _stream(stream))
+    f = getattr(_LIB or load(), what)
+    if stream is not None:
+        raw.append(_stream(stream))
+    else:
+        raw.append(torch._C._cuda_getCurrentRawStream(dev))
+    if dev == torch._C._cuda_getDevice():
+        rc = f(*raw)
     else:
         with torch.cuda.device(dev):
-            rc = f(*raw, _stream(stream))
+            rc = f(*raw)
     if rc != QE_OK:
         _check(rc, what)
 
 
 def _expect(t, dtype, shape, name: str):
     """Checks a tensor's type and shape (an int: its least number of elements) before its pointer is passed on."""
-    if t.dtype != dtype or (t.numel() < shape if isinstance(shape, int) else tuple(t.shape) != shape):
+    if t.dtype != dtype or (t.numel() < shape if isinstance(shape, int) else t.shape != shape):
         raise QEError(QE_ERR_INVALID_ARG, name, f"expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -394,6 +400,7 @@ def mx4_code_bytes(rows: int, cols: int) -> int:
     return int(load().qe_mx4_code_bytes(rows, cols))
 
 
+@functools.lru_cache(maxsize=1024)
 def mx4_scale_bytes(rows: int, cols: int) -> int:
     return int(load().qe_mx4_scale_bytes(rows, cols))
 
@@ -432,6 +439,7 @@ def mx4_product(x_codes, x_scales, w_codes, w_scales, Y, stream=None):
     _launch("qe_mx4_product", stream, x_codes, x_scales, w_codes, w_scales, T, K, N, Y, _dtype(Y))
 
 
+@functools.lru_cache(maxsize=1024)
 def mx4_linear_workspace_bytes(T: int, d_in: int) -> int:
     return int(load().qe_mx4_linear_workspace_bytes(T, d_in))
 

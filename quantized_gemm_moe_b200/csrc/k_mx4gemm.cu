@@ -182,6 +182,233 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// ------------------------------------------------------------------ many tokens
+// Y tile of 256 tokens x 256 output channels per pair of CTAs (cta_group::2: each CTA holds 128 token rows, half of
+// the weight rows and a 128 x 256 accumulator), persistent over the tiles. A tile reads 512 rows for 256 x 256
+// outputs, half of what the two CTAs would read as 128 x 256 tiles of their own: at the 4-bit rate the
+// shared memory fill is what limits smaller tiles.
+struct PairCfg {
+  static constexpr int kA = 16384, kB = 16384, kSA = 1024, kSB = 2048;
+  static constexpr int kStage = kA + kB + kSA + kSB;
+  static constexpr int kStages = 5;
+  // Tensor memory: two accumulators of 256 columns that share the columns [192, 256), and two sets of scales.
+  // The epilogue drains the shared columns first, so the next tile's MMAs start after a quarter of it.
+  static constexpr int kAcc1 = 192, kSf = 448, kSfCols = 24;
+  static constexpr int kPad = 33;  // row pitch of the transposing buffers
+  static constexpr int kTrans = 4 * 32 * kPad * 4;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kTrans + 256;
+  static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512, "layout");
+};
+constexpr int kPairThreads = 192;
+
+struct PairArgs {
+  int T, N, K, KT;
+  int m_tiles, n_tiles, group;  // group: token tiles walked together, so that their activations stay in L2
+  void* Y;
+  int y_bf16, vec;              // vec: rows of Y allow 32-byte stores
+  int* err;
+};
+
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& mt, int& nt) {
+  const int per = a.group * a.n_tiles, g = tile / per, r = tile - g * per;
+  const int rows = min(a.group, a.m_tiles - g * a.group);
+  mt = g * a.group + r % rows;
+  nt = r / rows;
+}
+
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    k_mx4_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+               const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws, const PairArgs a) {
+  using C = PairCfg;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* trans = reinterpret_cast<float*>(smem + NS * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * C::kStage + C::kTrans);
+  uint64_t* empty = full + NS;
+  uint64_t* accf = empty + NS;   // [2] a tile's MMAs are done
+  uint64_t* freed = accf + 2;    // the shared columns of a tile are drained (even CTA's, from both CTAs)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(freed + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int KS = (a.K + kMxStageK - 1) / kMxStageK;
+  const int tiles = a.m_tiles * a.n_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&accf[0], 1);
+    mbar_init(&accf[1], 1);
+    mbar_init(freed, 8);
+    mbar_fence_init();
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_xs);
+    prefetch_tmap(&tm_ws);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are ready before either's loads or arrivals reach them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        int mt, nt;
+        pair_tile(a, tile, mt, nt);
+        const int m0 = mt * 256 + cta * 128, n0 = nt * 256 + cta * 128;
+        for (int ks = 0; ks < KS; ++ks, ++it) {
+          const int s = it % NS;
+          if (!mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, a.err, DEVERR_WAIT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * C::kStage;
+          // the even CTA's barrier counts both CTAs' bytes
+          if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+          const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+          tma_load_2d_pair(st, &tm_x, ks * 128, m0, bar);
+          tma_load_2d_pair(st + C::kA, &tm_w, ks * 128, n0, bar);
+          tma_load_2d_pair(st + C::kA + C::kB, &tm_xs, ks * 256, mt * 2 + cta, bar);
+          tma_load_2d_pair(st + C::kA + C::kB + C::kSA, &tm_ws, ks * 256, nt * 2, bar);
+        }
+      }
+      if (cta == 0) drain_ring(full, NS, it);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (cta == 0) {
+      constexpr uint32_t id = idesc_mxf4(256, 256);
+      const bool leader = elect_one();
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs, ++n) {
+        if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(freed, (n - 1) & 1, a.err, DEVERR_WAIT_MMA))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + ((n & 1) ? C::kAcc1 : 0);
+        for (int ks = 0; ks < KS; ++ks, ++it) {
+          const int s = it % NS;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (it / NS) & 1, a.err, DEVERR_WAIT_MMA))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (leader) {
+            const uint32_t at = smem_u32(smem + s * C::kStage);
+            const uint32_t sfa = tmem + C::kSf + (it & 1) * C::kSfCols, sfb = sfa + 8;
+            const uint32_t sa = at + C::kA + C::kB, sb = sa + C::kSA;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              tmem_cp_32x128b_pair(sfa + 4 * k, smem_desc_rows16(sa + k * kMxTileBytes));
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                tmem_cp_32x128b_pair(sfb + (2 * k + b) * 4, smem_desc_rows16(sb + b * 1024 + k * kMxTileBytes));
+            }
+            const uint64_t da = smem_desc_sw128(at), db = smem_desc_sw128(at + C::kA);
+            const int mmas = min(4, (a.K - ks * kMxStageK + 63) / 64);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t sel = static_cast<uint32_t>(m & 1) * 2;
+              if (m < mmas)
+                mma_mxf4_pair(acc, da + 2 * m, db + 2 * m, id | (sel << 29) | (sel << 4), sfa + 4 * (m >> 1),
+                              sfb + 8 * (m >> 1), (ks | m) != 0);
+            }
+            tc_commit_pair(&empty[s]);
+            if (ks == KS - 1) tc_commit_pair(&accf[n & 1]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    float* tw = trans + q * 32 * C::kPad;
+    const uint32_t freed0 = mapa(smem_u32(freed), 0);
+    int n = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++n) {
+      int mt, nt;
+      pair_tile(a, tile, mt, nt);
+      if (!__all_sync(0xffffffffu, mbar_wait(&accf[n & 1], (n >> 1) & 1, a.err, DEVERR_WAIT_EPILOGUE))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((n & 1) ? C::kAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
+      const int row0 = mt * 256 + cta * 128 + 32 * q, n0 = nt * 256;
+      // chunks of 32 columns, the shared ones first: 6, 7, 0 .. 5 of the first accumulator, 0 .. 7 of the second
+      const int first = (n & 1) ? 0 : 6;
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        const int c = ((first + j) & 7) * 32;
+        uint32_t v[32];
+        tmem_ld32(acc + c, v);
+        tmem_wait_ld();
+        reg_fence(v);
+        if (j == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(freed0);
+        }
+        const int col = n0 + c;
+        if (a.vec && col + 32 <= a.N) {
+          if (row0 + lane < a.T) {
+            const size_t y = static_cast<size_t>(row0 + lane) * a.N + col;
+            if (a.y_bf16) {
+              uint32_t w[2][8];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                w[i >> 3][i & 7] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              st_global_32b(static_cast<uint16_t*>(a.Y) + y, w[0]);
+              st_global_32b(static_cast<uint16_t*>(a.Y) + y + 16, w[1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t w[8] = {v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
+                                       v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
+                st_global_32b(static_cast<float*>(a.Y) + y + 8 * i, w);
+              }
+            }
+          }
+        } else if (col < a.N) {
+          // rows that are no multiple of 32 bytes, or the last columns: through shared memory, a row per store
+#pragma unroll
+          for (int i = 0; i < 32; ++i) tw[lane * C::kPad + i] = __uint_as_float(v[i]);
+          __syncwarp();
+          const int rows = min(32, a.T - row0);
+          for (int r = 0; r < rows; ++r) {
+            const float f = tw[r * C::kPad + lane];
+            if (col + lane < a.N) {
+              const size_t y = static_cast<size_t>(row0 + r) * a.N + col + lane;
+              if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(f);
+              else static_cast<float*>(a.Y)[y] = f;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();  // neither CTA frees memory that the other's instructions may still use
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -215,18 +442,50 @@ cudaError_t launch_split_t(const CUtensorMap& tm_w, const CUtensorMap& tm_x, con
 
 Mx4Plan plan_mx4(int T, int N, int K) {
   Mx4Plan p{};
+  int sms = sm_count();
+  if (sms == 0) sms = 148;
+  p.pair = T > 256;
+  if (p.pair) {
+    p.bn = 256;
+    p.n_tiles = static_cast<int>(ceil_div(N, 256));
+    p.t_tiles = static_cast<int>(ceil_div(T, 256));
+    p.splits = 1;
+    p.ctas = static_cast<int>(2 * std::min<int64_t>(sms / 2, static_cast<int64_t>(p.n_tiles) * p.t_tiles));
+    return p;
+  }
   p.bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
   p.n_tiles = static_cast<int>(ceil_div(N, 128));
   p.t_tiles = static_cast<int>(ceil_div(T, p.bn));
   // as many CTAs as two per SM (one at 256 tokens) hold, in clusters of at most eight along K
-  int sms = sm_count();
-  if (sms == 0) sms = 148;
   const int slots = p.bn == 256 ? sms : 2 * sms;
   const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.t_tiles;
   const int stages = static_cast<int>(ceil_div(K, kMxStageK));
   p.splits = 1;
   while (p.splits < 8 && tiles * p.splits * 2 <= slots && p.splits * 2 <= stages) p.splits *= 2;
+  p.ctas = static_cast<int>(tiles * p.splits);
   return p;
+}
+
+cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const CUtensorMap& tm_ws,
+                            const CUtensorMap& tm_xs, const Mx4Plan& p, int T, int N, int K, void* Y, bool y_bf16,
+                            int* err, cudaStream_t st) {
+  using C = PairCfg;
+  cudaError_t e = cudaFuncSetAttribute(k_mx4_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  PairArgs a{};
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.KT = static_cast<int>(ceil_div(K, kMxTileCols));
+  a.m_tiles = p.t_tiles;
+  a.n_tiles = p.n_tiles;
+  a.group = std::min(p.t_tiles, 8);
+  a.Y = Y;
+  a.y_bf16 = y_bf16;
+  a.vec = (static_cast<size_t>(N) * (y_bf16 ? 2 : 4)) % 32 == 0 && reinterpret_cast<uintptr_t>(Y) % 32 == 0;
+  a.err = err;
+  k_mx4_pair<<<p.ctas, kPairThreads, C::kSmem, st>>>(tm_x, tm_w, tm_xs, tm_ws, a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_mx4_product(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,

@@ -142,9 +142,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D row-major [rows][cols] tensor, box {box_cols, box_rows}, 128-byte swizzle, zero fill out of bounds.
+// 2-D row-major [rows][cols] tensor, box {box_cols, box_rows}, zero fill out of bounds.
 qe_status make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t cols,
-                    uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
+                    uint64_t rows, uint32_t box_cols, uint32_t box_rows,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) {
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled unavailable");
@@ -155,7 +156,7 @@ qe_status make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled failed (%d)", int(r));
     return QE_ERR_CUDA;
@@ -386,6 +387,21 @@ qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void
   CUtensorMap tm_w, tm_x;
   qe_status s;
   if ((s = make_tmap(&tm_w, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, d_out, 128, 128)) != QE_OK) return s;
+  if (p.pair) {
+    // scale tiles as rows of 32-bit words: 512 bytes for each 128 channels, a row for each 128 rows
+    CUtensorMap tm_ws, tm_xs;
+    const uint64_t words = uint64_t(ceil_div(d_in, 128)) * 128;
+    if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128, 128)) != QE_OK) return s;
+    if ((s = make_tmap(&tm_ws, w_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, words, ceil_div(d_out, 128), 256, 2,
+                       CU_TENSOR_MAP_SWIZZLE_NONE)) != QE_OK)
+      return s;
+    if ((s = make_tmap(&tm_xs, x_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, words, ceil_div(T, 128), 256, 1,
+                       CU_TENSOR_MAP_SWIZZLE_NONE)) != QE_OK)
+      return s;
+    QE_CUDA(launch_mx4_pair(tm_w, tm_x, tm_ws, tm_xs, p, T, d_out, d_in, Y, yd == QE_BF16, device_error_ptr(), st),
+            "mx4_pair");
+    return QE_OK;
+  }
   if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128, p.bn)) != QE_OK) return s;
   QE_CUDA(launch_mx4_product(tm_w, tm_x, p, static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(x_scales),
                              T, d_out, d_in, Y, yd == QE_BF16, device_error_ptr(), st),
