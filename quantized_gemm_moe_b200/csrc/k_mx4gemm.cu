@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
 // outputs, half of what the two CTAs would read as 128 x 256 tiles of their own: at the 4-bit rate the
 // shared memory fill is what limits smaller tiles.
 struct PairCfg {
+  static constexpr int kEpiWarps = 8;  // two for each 32 token rows, alternate chunks of 32 columns
   static constexpr int kA = 16384, kB = 16384, kSA = 1024, kSB = 2048;
   static constexpr int kStage = kA + kB + kSA + kSB;
   static constexpr int kStages = 5;
@@ -195,11 +196,11 @@ struct PairCfg {
   // The epilogue drains the shared columns first, so the next tile's MMAs start after a quarter of it.
   static constexpr int kAcc1 = 192, kSf = 448, kSfCols = 24;
   static constexpr int kPad = 33;  // row pitch of the transposing buffers
-  static constexpr int kTrans = 4 * 32 * kPad * 4;
+  static constexpr int kTrans = kEpiWarps * 32 * kPad * 4;
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kTrans + 256;
   static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512, "layout");
 };
-constexpr int kPairThreads = 192;
+constexpr int kPairThreads = 64 + 32 * PairCfg::kEpiWarps;
 
 struct PairArgs {
   int T, N, K, KT;
@@ -220,6 +221,48 @@ __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// Stores a warp's 32 rows x 32 columns of Y from its registers (v: this lane's row).
+__device__ __forceinline__ void pair_store(const PairArgs& a, const uint32_t (&v)[32], int row0, int col, int lane,
+                                           float* tw) {
+  if (a.vec && col + 32 <= a.N) {
+    if (row0 + lane < a.T) {
+      const size_t y = static_cast<size_t>(row0 + lane) * a.N + col;
+      if (a.y_bf16) {
+        uint32_t w[2][8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          w[i >> 3][i & 7] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        st_global_32b(static_cast<uint16_t*>(a.Y) + y, w[0]);
+        st_global_32b(static_cast<uint16_t*>(a.Y) + y + 16, w[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[8] = {v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
+                                 v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
+          st_global_32b(static_cast<float*>(a.Y) + y + 8 * i, w);
+        }
+      }
+    }
+  } else if (col < a.N) {
+    // rows that are no multiple of 32 bytes, or the last columns: through shared memory, a row per store
+#pragma unroll
+    for (int i = 0; i < 32; ++i) tw[lane * PairCfg::kPad + i] = __uint_as_float(v[i]);
+    __syncwarp();
+    const int rows = min(32, a.T - row0);
+    for (int r = 0; r < rows; ++r) {
+      const float f = tw[r * PairCfg::kPad + lane];
+      if (col + lane < a.N) {
+        const size_t y = static_cast<size_t>(row0 + r) * a.N + col + lane;
+        if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(f);
+        else static_cast<float*>(a.Y)[y] = f;
+      }
+    }
+    __syncwarp();
+  }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
@@ -248,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     }
     mbar_init(&accf[0], 1);
     mbar_init(&accf[1], 1);
-    mbar_init(freed, 8);
+    mbar_init(freed, 2 * C::kEpiWarps);
     mbar_fence_init();
     prefetch_tmap(&tm_x);
     prefetch_tmap(&tm_w);
@@ -337,8 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       }
     }
   } else {
-    const int q = warp & 3;
-    float* tw = trans + q * 32 * C::kPad;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    float* tw = trans + (warp - 2) * 32 * C::kPad;
     const uint32_t freed0 = mapa(smem_u32(freed), 0);
     int n = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++n) {
@@ -349,57 +392,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       const uint32_t acc = tmem + ((n & 1) ? C::kAcc1 : 0) + (static_cast<uint32_t>(32 * q) << 16);
       const int row0 = mt * 256 + cta * 128 + 32 * q, n0 = nt * 256;
       // chunks of 32 columns, the shared ones first: 6, 7, 0 .. 5 of the first accumulator, 0 .. 7 of the second
-      const int first = (n & 1) ? 0 : 6;
+      const int first = ((n & 1) ? 0 : 6) + half;
 #pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 8; j += 2) {
         const int c = ((first + j) & 7) * 32;
         uint32_t v[32];
         tmem_ld32(acc + c, v);
         tmem_wait_ld();
         reg_fence(v);
-        if (j == 1) {
+        if (j == 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(freed0);
+          if (lane == 0) mbar_arrive_cluster_relaxed(freed0);
         }
-        const int col = n0 + c;
-        if (a.vec && col + 32 <= a.N) {
-          if (row0 + lane < a.T) {
-            const size_t y = static_cast<size_t>(row0 + lane) * a.N + col;
-            if (a.y_bf16) {
-              uint32_t w[2][8];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                w[i >> 3][i & 7] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              st_global_32b(static_cast<uint16_t*>(a.Y) + y, w[0]);
-              st_global_32b(static_cast<uint16_t*>(a.Y) + y + 16, w[1]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t w[8] = {v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
-                                       v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
-                st_global_32b(static_cast<float*>(a.Y) + y + 8 * i, w);
-              }
-            }
-          }
-        } else if (col < a.N) {
-          // rows that are no multiple of 32 bytes, or the last columns: through shared memory, a row per store
-#pragma unroll
-          for (int i = 0; i < 32; ++i) tw[lane * C::kPad + i] = __uint_as_float(v[i]);
-          __syncwarp();
-          const int rows = min(32, a.T - row0);
-          for (int r = 0; r < rows; ++r) {
-            const float f = tw[r * C::kPad + lane];
-            if (col + lane < a.N) {
-              const size_t y = static_cast<size_t>(row0 + r) * a.N + col + lane;
-              if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(f);
-              else static_cast<float*>(a.Y)[y] = f;
-            }
-          }
-          __syncwarp();
-        }
+        pair_store(a, v, row0, n0 + c, lane, tw);
       }
     }
     tc_fence_before();
