@@ -195,10 +195,14 @@ struct PairCfg {
   // Tensor memory: two accumulators of 256 columns that share the columns [192, 256), and two sets of scales.
   // The epilogue drains the shared columns first, so the next tile's MMAs start after a quarter of it.
   static constexpr int kAcc1 = 192, kSf = 448, kSfCols = 24;
-  static constexpr int kPad = 33;  // row pitch of the transposing buffers
-  static constexpr int kTrans = kEpiWarps * 32 * kPad * 4;
+  // An epilogue warp's staging buffer: a 32 x 32 block of Y, swizzled for its TMA store (two of them in bf16), or
+  // padded rows of fp32 where Y's rows allow no TMA store.
+  static constexpr int kPad = 33;
+  static constexpr int kOut = 5120;
+  static constexpr int kTrans = kEpiWarps * kOut;
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kTrans + 256;
-  static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512, "layout");
+  static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512 && 32 * kPad * 4 <= kOut, "layout");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr int kPairThreads = 64 + 32 * PairCfg::kEpiWarps;
 
@@ -206,7 +210,7 @@ struct PairArgs {
   int T, N, K, KT;
   int m_tiles, n_tiles, group;  // group: token tiles walked together, so that their activations stay in L2
   void* Y;
-  int y_bf16, vec;              // vec: rows of Y allow 32-byte stores
+  int y_bf16, tma;              // tma: Y's rows are multiples of 16 bytes
   int* err;
 };
 
@@ -217,38 +221,54 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& mt, 
   nt = r / rows;
 }
 
-__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// Stores a warp's 32 rows x 32 columns of Y from its registers (v: this lane's row).
-__device__ __forceinline__ void pair_store(const PairArgs& a, const uint32_t (&v)[32], int row0, int col, int lane,
-                                           float* tw) {
-  if (a.vec && col + 32 <= a.N) {
-    if (row0 + lane < a.T) {
-      const size_t y = static_cast<size_t>(row0 + lane) * a.N + col;
-      if (a.y_bf16) {
-        uint32_t w[2][8];
+// Stores a warp's 32 rows x 32 columns of Y from its registers (v: this lane's row). `turn` counts the warp's
+// TMA stores: a staging half is written again once the store before last (bf16) or the last (fp32) has
+// read it.
+__device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap* tm_y, const uint32_t (&v)[32], int row0,
+                                           int col, int lane, uint8_t* out, int& turn) {
+  if (a.tma) {
+    if (col >= a.N || row0 >= a.T) return;
+    if (a.y_bf16) {
+      // rows of 64 bytes, 16-byte pieces permuted by bits 7-8 of their offset (64-byte swizzle)
+      uint8_t* half = out + (turn & 1) * 2048;
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          w[i >> 3][i & 7] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        st_global_32b(static_cast<uint16_t*>(a.Y) + y, w[0]);
-        st_global_32b(static_cast<uint16_t*>(a.Y) + y + 16, w[1]);
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w[8] = {v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
-                                 v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]};
-          st_global_32b(static_cast<float*>(a.Y) + y + 8 * i, w);
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 h =
+              __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        *reinterpret_cast<uint4*>(half + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tm_y, half, col, row0);
+        bulk_commit();
+      }
+    } else {
+      // rows of 128 bytes, pieces permuted by bits 7-9 (128-byte swizzle)
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(out + lane * 128 + (i ^ (lane & 7)) * 16) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tm_y, out, col, row0);
+        bulk_commit();
       }
     }
+    ++turn;
   } else if (col < a.N) {
-    // rows that are no multiple of 32 bytes, or the last columns: through shared memory, a row per store
+    // through shared memory, a row per store
+    float* tw = reinterpret_cast<float*>(out);
 #pragma unroll
     for (int i = 0; i < 32; ++i) tw[lane * PairCfg::kPad + i] = __uint_as_float(v[i]);
     __syncwarp();
@@ -267,12 +287,13 @@ __device__ __forceinline__ void pair_store(const PairArgs& a, const uint32_t (&v
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     k_mx4_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-               const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws, const PairArgs a) {
+               const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
+               const __grid_constant__ CUtensorMap tm_y, const PairArgs a) {
   using C = PairCfg;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* trans = reinterpret_cast<float*>(smem + NS * C::kStage);
+  uint8_t* staging = smem + NS * C::kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * C::kStage + C::kTrans);
   uint64_t* empty = full + NS;
   uint64_t* accf = empty + NS;   // [2] a tile's MMAs are done
@@ -297,6 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_xs);
     prefetch_tmap(&tm_ws);
+    prefetch_tmap(&tm_y);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -381,7 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    float* tw = trans + (warp - 2) * 32 * C::kPad;
+    uint8_t* out = staging + (warp - 2) * C::kOut;
+    int turn = 0;
     const uint32_t freed0 = mapa(smem_u32(freed), 0);
     int n = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++n) {
@@ -405,9 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(freed0);
         }
-        pair_store(a, v, row0, n0 + c, lane, tw);
+        pair_store(a, &tm_y, v, row0, n0 + c, lane, out, turn);
       }
     }
+    if (lane == 0) bulk_wait_all();
     tc_fence_before();
   }
   __syncthreads();
@@ -473,8 +497,8 @@ Mx4Plan plan_mx4(int T, int N, int K) {
 }
 
 cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const CUtensorMap& tm_ws,
-                            const CUtensorMap& tm_xs, const Mx4Plan& p, int T, int N, int K, void* Y, bool y_bf16,
-                            int* err, cudaStream_t st) {
+                            const CUtensorMap& tm_xs, const CUtensorMap* tm_y, const Mx4Plan& p, int T, int N, int K,
+                            void* Y, bool y_bf16, int* err, cudaStream_t st) {
   using C = PairCfg;
   cudaError_t e = cudaFuncSetAttribute(k_mx4_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
@@ -488,9 +512,9 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
   a.group = std::min(p.t_tiles, 8);
   a.Y = Y;
   a.y_bf16 = y_bf16;
-  a.vec = (static_cast<size_t>(N) * (y_bf16 ? 2 : 4)) % 32 == 0 && reinterpret_cast<uintptr_t>(Y) % 32 == 0;
+  a.tma = tm_y != nullptr;
   a.err = err;
-  k_mx4_pair<<<p.ctas, kPairThreads, C::kSmem, st>>>(tm_x, tm_w, tm_xs, tm_ws, a);
+  k_mx4_pair<<<p.ctas, kPairThreads, C::kSmem, st>>>(tm_x, tm_w, tm_xs, tm_ws, tm_y ? *tm_y : tm_x, a);
   return cudaGetLastError();
 }
 

@@ -244,7 +244,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
                                   bool out_bf16, cudaStream_t st);
 
 // How the MXFP4 product runs. pair: persistent pairs of CTAs over tiles of 256 tokens x 256 output channels; all
-// boxes are 128 rows of codes, tm_ws 2 and tm_xs 1 rows of scale tiles. Otherwise tiles of 128 output
+// boxes are 128 rows of codes, tm_ws 2 and tm_xs 1 rows of scale tiles, tm_y 32 x 32 elements (null where Y's rows are
+// no multiple of 16 bytes). Otherwise tiles of 128 output
 // channels x bn tokens, K split over clusters of `splits` CTAs; tm_w boxes are 128 rows, tm_x boxes bn.
 struct Mx4Plan {
   bool pair;
@@ -252,8 +253,8 @@ struct Mx4Plan {
 };
 Mx4Plan plan_mx4(int T, int N, int K);
 cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const CUtensorMap& tm_ws,
-                            const CUtensorMap& tm_xs, const Mx4Plan& p, int T, int N, int K, void* Y, bool y_bf16,
-                            int* err, cudaStream_t st);
+                            const CUtensorMap& tm_xs, const CUtensorMap* tm_y, const Mx4Plan& p, int T, int N, int K,
+                            void* Y, bool y_bf16, int* err, cudaStream_t st);
 cudaError_t launch_mx4_product(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
                                const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, int* err,
                                cudaStream_t st);
