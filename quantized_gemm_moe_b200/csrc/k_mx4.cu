@@ -9,72 +9,102 @@ namespace qe {
 namespace {
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantIters = 4;                        // 256-channel pieces of a row per warp
-constexpr int kQuantSpan = 256 * kQuantIters;         // channels per warp
+constexpr int kLaneK = 8;                             // channels per lane and step: a quarter of a block
+constexpr int kStepK = 32 * kLaneK;                   // channels per warp and step
+constexpr int kQuantSteps = 2;
+constexpr int kQuantRows = 2;                         // neighbouring rows per warp: they share the factors s
+constexpr int kQuantSpan = kStepK * kQuantSteps;      // channels per warp
 
-// A warp takes 1024 neighbouring channels of a row: eight per lane and piece, so every load is 512
-// contiguous bytes of bf16 (1 KB of fp32) and every store of codes 128. All loads are in flight before
-// the first is used. HBM bound: 2 (4) bytes read and 0.53 written for each element.
-template <bool BF16>
+// A warp takes 512 neighbouring channels of two rows: eight per lane and step, four lanes to a block, so that a
+// step reads 512 contiguous bytes of bf16 (1 KB of fp32) and writes 128 of codes. All loads of x are in flight
+// before the first is used. HBM: 2 (4) bytes read and 0.53 written for each element; what comes next is L1,
+// which the factors s (1 KB a step) load more than bf16 rows do, hence two rows. 29568 x 8192 bf16 with s:
+// 104 us, 5.9 TB/s (one row and 1024 channels: 111 us).
+// FULL: the warp's channels and rows all exist (nothing is predicated).
+template <bool BF16, bool SMOOTH, bool FULL>
+__device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, size_t pitch, const float* __restrict__ s,
+                                              int k0, int cols, int rows, int lane, uint8_t* __restrict__ c,
+                                              uint8_t* __restrict__ sc0, uint8_t* __restrict__ sc1) {
+  constexpr int kE = BF16 ? 2 : 4;
+  uint4 raw[kQuantSteps][kQuantRows][kE / 2];
+#pragma unroll
+  for (int j = 0; j < kQuantSteps; ++j) {
+#pragma unroll
+    for (int r = 0; r < kQuantRows; ++r) {
+      if (FULL || (k0 + kStepK * j < cols && r < rows)) {
+#pragma unroll
+        for (int h = 0; h < kE / 2; ++h)
+          raw[j][r][h] = __ldg(reinterpret_cast<const uint4*>(x + r * pitch * kE + kStepK * kE * j) + h);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kQuantSteps; ++j) {
+    const int k = k0 + kStepK * j;
+    float f[8];
+    if (SMOOTH && (FULL || k < cols)) {
+      const float4 f0 = __ldg(reinterpret_cast<const float4*>(s + kStepK * j));
+      const float4 f1 = __ldg(reinterpret_cast<const float4*>(s + kStepK * j) + 1);
+      f[0] = f0.x; f[1] = f0.y; f[2] = f0.z; f[3] = f0.w;
+      f[4] = f1.x; f[5] = f1.y; f[6] = f1.z; f[7] = f1.w;
+    }
+#pragma unroll
+    for (int r = 0; r < kQuantRows; ++r) {
+      const bool valid = FULL || (k < cols && r < rows);
+      float v[8];
+      if (valid) {
+        const uint4 p = raw[j][r][0], q = raw[j][r][kE / 2 - 1];
+        if constexpr (BF16) {
+          const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          }
+        } else {
+          const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        }
+        if constexpr (SMOOTH) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], f[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      }
+      uint32_t top = absmax8(v);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t byte = mx_scale_byte(top);
+      const uint32_t code = mx_codes8(v, byte);
+      if (valid) *reinterpret_cast<uint32_t*>(c + r * pitch / 2 + kStepK / 2 * j) = code;
+      if ((lane & 3) == 0 && (FULL || (k < static_cast<int>(round_up(cols, kMxTileCols)) && r < rows)))
+        (r ? sc1 : sc0)[kStepK / kMxTileCols * kMxTileBytes * j] = static_cast<uint8_t>(valid ? byte : kMxOne);
+    }
+  }
+}
+
+template <bool BF16, bool SMOOTH>
 __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const void* __restrict__ X, const float* __restrict__ s,
-                                                                int cols, int spans, size_t units,
+                                                                int rows, int cols, int spans, size_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
-  const size_t row = unit / spans;
-  const int k0 = static_cast<int>(unit - row * spans) * kQuantSpan + lane * 8;
-  const size_t base = row * cols, KT = (cols + kMxTileCols - 1) / kMxTileCols;
-  uint4 raw[kQuantIters][BF16 ? 1 : 2];
-#pragma unroll
-  for (int j = 0; j < kQuantIters; ++j) {
-    const int k = k0 + 256 * j;
-    if (k < cols) {
-      if constexpr (BF16) {
-        raw[j][0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + base + k));
-      } else {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + base + k);
-        raw[j][0] = __ldg(q);
-        raw[j][1] = __ldg(q + 1);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kQuantIters; ++j) {
-    const int k = k0 + 256 * j;
-    float v[8];
-    if (k < cols) {
-      if constexpr (BF16) {
-        const uint32_t w[4] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-          v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-        }
-      } else {
-        const uint4 p = raw[j][0], q = raw[j][1];
-        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-      }
-      if (s) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(s + k)), b = __ldg(reinterpret_cast<const float4*>(s + k) + 1);
-        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], f[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
-    uint32_t word;
-    const uint32_t c = mx_quantize8(v, k < cols, lane, word);
-    if (k < cols) {
-      *reinterpret_cast<uint32_t*>(codes + (base + k) / 2) = c;
-      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(row, k / kMxTileCols, KT)) = word;
-    }
-  }
+  const size_t pair = unit / spans, row = pair * kQuantRows;
+  const int span0 = static_cast<int>(unit - pair * spans) * kQuantSpan, k0 = span0 + lane * kLaneK;
+  const size_t at = row * cols + k0;
+  const uint8_t* x = static_cast<const uint8_t*>(X) + at * (BF16 ? 2 : 4);
+  const int KT = (cols + kMxTileCols - 1) / kMxTileCols, left = static_cast<int>(rows - row);
+  uint8_t* sc0 = scales + mx_scale_row(row, KT) + mx_scale_at(k0);
+  uint8_t* sc1 = scales + mx_scale_row(row + 1, KT) + mx_scale_at(k0);
+  if (span0 + kQuantSpan <= cols && left >= kQuantRows)
+    quantize_span<BF16, SMOOTH, true>(x, cols, s + k0, k0, cols, left, lane, codes + at / 2, sc0, sc1);
+  else
+    quantize_span<BF16, SMOOTH, false>(x, cols, s + k0, k0, cols, left, lane, codes + at / 2, sc0, sc1);
 }
 
 // Two E2M1 codes (the low byte of c) as fp32.
@@ -88,8 +118,9 @@ __device__ __forceinline__ float2 e2m1x2(uint32_t c) {
   return f;
 }
 
-// The values of the codes, eight channels per lane as above. Every value has two significant bits, so
+// The values of the codes, eight channels per lane and step. Every value has two significant bits, so
 // it is exact in bf16 and fp32 (2^-128, the smallest, is a subnormal of both).
+constexpr int kDequantSpan = 1024;  // channels per warp
 __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, int cols,
                                                                   int spans, size_t units, void* __restrict__ out,
@@ -98,19 +129,21 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t*
   const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
   const size_t row = unit / spans;
-  const int k0 = static_cast<int>(unit - row * spans) * kQuantSpan + lane * 8;
-  const size_t base = row * cols, KT = (cols + kMxTileCols - 1) / kMxTileCols;
-  uint32_t c[kQuantIters], b[kQuantIters];
+  constexpr int kSteps = kDequantSpan / 256;
+  const int k0 = static_cast<int>(unit - row * spans) * kDequantSpan + lane * 8;
+  const size_t base = row * cols;
+  const uint8_t* sc = scales + mx_scale_row(row, (cols + kMxTileCols - 1) / kMxTileCols);
+  uint32_t c[kSteps], b[kSteps];
 #pragma unroll
-  for (int j = 0; j < kQuantIters; ++j) {
+  for (int j = 0; j < kSteps; ++j) {
     const int k = k0 + 256 * j;
     if (k < cols) {
       c[j] = __ldg(reinterpret_cast<const uint32_t*>(codes + (base + k) / 2));
-      b[j] = __ldg(scales + mx_scale_word(row, k / kMxTileCols, KT) + k % kMxTileCols / kMxBlock);
+      b[j] = __ldg(sc + mx_scale_at(k));
     }
   }
 #pragma unroll
-  for (int j = 0; j < kQuantIters; ++j) {
+  for (int j = 0; j < kSteps; ++j) {
     const int k = k0 + 256 * j;
     if (k >= cols) break;
     const float e = mx_scale(b[j]);
@@ -124,9 +157,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t*
     if (out_bf16) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i])) |
-               (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16);
+      for (int i = 0; i < 4; ++i) w[i] = bf16x2_word(v[2 * i], v[2 * i + 1]);
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + base + k) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + base + k);
@@ -142,17 +173,18 @@ cudaError_t launch_mx4_quantize(const void* X, bool x_bf16, const float* s, int 
                                 uint8_t* scales, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const int spans = static_cast<int>(ceil_div(cols, kQuantSpan));
-  const size_t units = static_cast<size_t>(rows) * spans;
+  const size_t units = static_cast<size_t>(ceil_div(rows, kQuantRows)) * spans;
   const unsigned grid = static_cast<unsigned>(ceil_div(units, kQuantThreads / 32));
-  if (x_bf16) k_mx4_quantize<true><<<grid, kQuantThreads, 0, st>>>(X, s, cols, spans, units, codes, scales);
-  else k_mx4_quantize<false><<<grid, kQuantThreads, 0, st>>>(X, s, cols, spans, units, codes, scales);
+  auto k = x_bf16 ? (s ? k_mx4_quantize<true, true> : k_mx4_quantize<true, false>)
+                  : (s ? k_mx4_quantize<false, true> : k_mx4_quantize<false, false>);
+  k<<<grid, kQuantThreads, 0, st>>>(X, s, rows, cols, spans, units, codes, scales);
   return cudaGetLastError();
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
                                   bool out_bf16, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  const int spans = static_cast<int>(ceil_div(cols, kQuantSpan));
+  const int spans = static_cast<int>(ceil_div(cols, kDequantSpan));
   const size_t units = static_cast<size_t>(rows) * spans;
   k_mx4_dequantize<<<static_cast<unsigned>(ceil_div(units, kQuantThreads / 32)), kQuantThreads, 0, st>>>(
       codes, scales, cols, spans, units, out, out_bf16);

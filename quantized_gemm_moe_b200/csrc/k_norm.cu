@@ -45,9 +45,7 @@ __device__ __forceinline__ void st8(void* p, size_t i, bool bf16, const float (&
   if (bf16) {
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * j])) |
-             (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * j + 1])) << 16);
+    for (int j = 0; j < 4; ++j) w[j] = bf16x2_word(v[2 * j], v[2 * j + 1]);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
@@ -130,10 +128,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(h[j][i], s[i]);
       }
-      if (OUT == kOutInt8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[j][i]) & 0x7FFFFFFFu);
-      }
+      if (OUT == kOutInt8) top = max(top, absmax8(h[j]));
     }
   }
   if (OUT == kOutInt8) {
@@ -152,41 +147,55 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const NormArgs a) {
       const int k = (tid + j * nt) * 8;
       if (k < a.d) {
         uint32_t w0 = 0, w1 = 0;
-        if (finite) rtn_code8(h[j], sa, inv, fast, a.qmax, w0, w1);
+        if (finite) rtn_code8_row(h[j], sa, inv, fast, a.qmax, w0, w1);
         *reinterpret_cast<uint2*>(a.codes + base + k) = make_uint2(w0, w1);
       }
     }
   }
   if (OUT == kOutMx4) {
-    const size_t KT = (a.d + kMxTileCols - 1) / kMxTileCols;
+    // four neighbouring lanes hold a block (rows are whole blocks); the first writes its scale
+    const int KT = (a.d + kMxTileCols - 1) / kMxTileCols;
+    uint8_t* sc = static_cast<uint8_t*>(a.scales) + mx_scale_row(row, KT);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int k = (tid + j * nt) * 8;
-      uint32_t word;
-      const uint32_t c = mx_quantize8(h[j], k < a.d, lane, word);
-      if (k < a.d) {
-        *reinterpret_cast<uint32_t*>(a.codes + (base + k) / 2) = c;
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + mx_scale_word(row, k / kMxTileCols, KT)) = word;
-      }
+      uint32_t t = k < a.d ? absmax8(h[j]) : 0u;
+      t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      const uint32_t byte = mx_scale_byte(t);
+      if (k < a.d) *reinterpret_cast<uint32_t*>(a.codes + (base + k) / 2) = mx_codes8(h[j], byte);
+      if ((lane & 3) == 0 && k < KT * kMxTileCols) sc[mx_scale_at(k)] = static_cast<uint8_t>(k < a.d ? byte : kMxOne);
     }
   }
 }
 
-// out[t][k] = codes[t][k] * sa[t], eight channels per thread.
+// out[t][k] = codes[t][k] * sa[t], eight channels per thread and step, four steps in flight.
+constexpr int kDequantSteps = 4;
 __global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ codes, const float* __restrict__ sa,
-                                                     int d8, size_t n8, void* __restrict__ out, int out_bf16) {
-  const size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x;
-  if (i >= n8) return;
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-  const float s = __ldg(sa + i / d8);
-  float v[8];
+                                                     uint32_t d8, uint32_t n8, void* __restrict__ out, int out_bf16) {
+  const uint32_t i0 = blockIdx.x * (256u * kDequantSteps) + threadIdx.x;
+  uint2 w[kDequantSteps];
+  float s[kDequantSteps];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = static_cast<float>(static_cast<int8_t>(w.x >> (8 * j))) * s;
-    v[4 + j] = static_cast<float>(static_cast<int8_t>(w.y >> (8 * j))) * s;
+  for (int j = 0; j < kDequantSteps; ++j) {
+    const uint32_t i = i0 + 256u * j;
+    if (i < n8) {
+      w[j] = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+      s[j] = __ldg(sa + i / d8);
+    }
   }
-  st8(out, i * 8, out_bf16, v);
+#pragma unroll
+  for (int j = 0; j < kDequantSteps; ++j) {
+    const uint32_t i = i0 + 256u * j;
+    if (i >= n8) break;
+    float v[8];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      v[b] = static_cast<float>(static_cast<int8_t>(w[j].x >> (8 * b))) * s[j];
+      v[4 + b] = static_cast<float>(static_cast<int8_t>(w[j].y >> (8 * b))) * s[j];
+    }
+    st8(out, static_cast<size_t>(i) * 8, out_bf16, v);
+  }
 }
 
 template <bool BF16, int VPT, int MAXT>
@@ -235,7 +244,9 @@ cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int 
                                cudaStream_t st) {
   const size_t n8 = static_cast<size_t>(T) * (d / 8);
   if (n8 == 0) return cudaSuccess;
-  k_act_dequant<<<static_cast<unsigned>(ceil_div(n8, 256)), 256, 0, st>>>(codes, sa, d / 8, n8, out, out_bf16);
+  if (n8 > 0xFFFF0000u) return cudaErrorInvalidValue;  // 32 G elements
+  k_act_dequant<<<static_cast<unsigned>(ceil_div(n8, 256 * kDequantSteps)), 256, 0, st>>>(
+      codes, sa, static_cast<uint32_t>(d / 8), static_cast<uint32_t>(n8), out, out_bf16);
   return cudaGetLastError();
 }
 

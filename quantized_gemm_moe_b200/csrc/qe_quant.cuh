@@ -81,13 +81,17 @@ constexpr int kMxBlock = 32;
 constexpr int kMxTileRows = 128;   // rows and
 constexpr int kMxTileCols = 128;   // channels of a tile of scale bytes (512 bytes)
 constexpr int kMxTileBytes = 512;
-constexpr uint32_t kMxOnes = 0x7F7F7F7Fu;  // four scales of one
+constexpr uint32_t kMxOne = 127u;  // a scale of one: what blocks past a row's end hold
 
-// Byte offset of the four scales of row r, channels [128*kt, 128*kt + 128); KT = ceil(cols / 128).
-// The order inside a tile is the one tcgen05.cp 32x128b spreads over the tensor memory lanes: 16 bytes
-// for each row r % 32, four for each r / 32.
-__host__ __device__ __forceinline__ size_t mx_scale_word(size_t r, size_t kt, size_t KT) {
-  return ((r >> 7) * KT + kt) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+// Byte offset of row r's four scales in the first of its KT = ceil(cols / 128) tiles; those of channels
+// [128*kt, 128*kt + 128) are kt * 512 bytes on. The order inside a tile is the one tcgen05.cp 32x128b
+// spreads over the tensor memory lanes: 16 bytes for each row r % 32, four for each r / 32.
+__host__ __device__ __forceinline__ size_t mx_scale_row(size_t r, size_t KT) {
+  return (r >> 7) * KT * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+// Offset of channel k's scale from there.
+__host__ __device__ __forceinline__ int mx_scale_at(int k) {
+  return (k / kMxTileCols) * kMxTileBytes + k % kMxTileCols / kMxBlock;
 }
 
 // Scale byte of a block whose largest |v| has the bits `top` (fp32, sign cleared).
@@ -117,26 +121,79 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float (&a)[8]) {
   return w;
 }
 
-// MXFP4 of 8 values per lane: four neighbouring lanes hold a block. Every lane of the warp calls it; a
-// lane past the row's end passes zeros and valid = false. Returns this lane's eight codes; `word`
-// receives the scale bytes of the 16-lane group's four blocks (127, a scale of one, for absent ones).
-// v * 2^-E is exact unless it falls below fp32's normal range, where the code is 0 either way.
-__device__ __forceinline__ uint32_t mx_quantize8(const float (&v)[8], bool valid, int lane, uint32_t& word) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const uint32_t byte = mx_scale_byte(top);
-  uint32_t w = (valid ? byte : 127u) << (8 * ((lane >> 2) & 3));
-  w |= __shfl_xor_sync(0xffffffffu, w, 4);
-  w |= __shfl_xor_sync(0xffffffffu, w, 8);
-  word = w;
-  const float inv = mx_inv_scale(byte == 255u ? 127u : byte);
+// The bits of max |v[i]|; those of a NaN (0x7FFFFFFF, above infinity's) when one is among them.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
+  float m = max3_abs(v[0], v[1], v[2]);
+  m = max3_abs(m, v[3], v[4]);
+  m = max3_abs(m, v[5], v[6]);
+  return __float_as_uint(max3_abs(m, v[7], v[7]));
+}
+
+// Codes of eight values of a block whose scale byte is `byte`. v * 2^-E is exact unless it falls below
+// fp32's normal range, where the code is 0 either way.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
+  const float inv = mx_inv_scale(byte);
   float a[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = v[i] * inv;
   return byte == 255u ? 0u : e2m1_pack8(a);
+}
+
+// rtn_code8 for a row whose scale came from its own finite absmax, so that |v * inv| <= qmax (1 + 2^-22) and the
+// clamp cannot bind.
+__device__ __forceinline__ void rtn_code8_row(const float (&v)[8], float scale, float inv, bool fast, int qmax,
+                                              uint32_t& w0, uint32_t& w1) {
+  constexpr float kM = 12582912.0f;
+  uint32_t b[8];
+  float d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float g = __fmul_rn(v[i], inv);
+    const float t = __fadd_rn(g, kM);
+    d[i] = __fmaf_rn(fabsf(g), 9.5367431640625e-07f, fabsf(__fsub_rn(g, __fsub_rn(t, kM))));
+    b[i] = __float_as_uint(t);
+  }
+  if (fast && absmax8(d) < 0x3F000000u) {  // every distance to rint(g), with its margin, below 0.5
+    w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    return;
+  }
+  const uint2 w = rtn_code8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], scale, qmax);
+  w0 = w.x;
+  w1 = w.y;
+}
+
+// 32 bytes at p: one load where p is 32-byte aligned, else two.
+__device__ __forceinline__ void ldg_32b(const void* p, bool aligned32, uint32_t (&w)[8]) {
+  if (aligned32) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void stg_32b(void* p, bool aligned32, const uint32_t (&w)[8]) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// Two fp32 values as a word of bf16 (the first in the low half).
+__device__ __forceinline__ uint32_t bf16x2_word(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 }  // namespace qe
