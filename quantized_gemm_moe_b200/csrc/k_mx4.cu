@@ -19,7 +19,7 @@ constexpr int kQuantSpan = kStepK * kQuantSteps;      // channels per warp
 // step reads 512 contiguous bytes of bf16 (1 KB of fp32) and writes 128 of codes. All loads of x are in flight
 // before the first is used. HBM: 2 (4) bytes read and 0.53 written for each element; what comes next is L1,
 // which the factors s (1 KB a step) load more than bf16 rows do, hence two rows. 29568 x 8192 bf16 with s:
-// 104 us, 5.9 TB/s (one row and 1024 channels: 111 us).
+// 101 us, 6.1 TB/s (one row and 1024 channels: 111 us).
 // FULL: the warp's channels and rows all exist (nothing is predicated).
 template <bool BF16, bool SMOOTH, bool FULL>
 __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, size_t pitch, const float* __restrict__ s,

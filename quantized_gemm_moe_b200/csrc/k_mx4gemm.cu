@@ -439,13 +439,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n;
-}
-
 template <int BN>
 cudaError_t launch_split_t(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const MxArgs& a, const Mx4Plan& p,
                            cudaStream_t st) {
@@ -472,7 +465,7 @@ cudaError_t launch_split_t(const CUtensorMap& tm_w, const CUtensorMap& tm_x, con
 
 Mx4Plan plan_mx4(int T, int N, int K) {
   Mx4Plan p{};
-  int sms = sm_count();
+  int sms = decode_grid_sms();
   if (sms == 0) sms = 148;
   p.pair = T > 256;
   if (p.pair) {

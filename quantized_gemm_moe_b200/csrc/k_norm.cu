@@ -1,7 +1,5 @@
 // The residual's addition and the root-mean-square norm in front of a quantized projection, with the
 // normed row quantized in the same pass, and the dequantization of per-token int8 codes.
-#include <algorithm>
-
 #include "qe_internal.h"
 #include "qe_ptx.cuh"
 #include "qe_quant.cuh"
@@ -15,7 +13,7 @@ struct NormArgs {
   const void* gamma;
   const float* s_inv;  // or nullptr
   double eps;
-  int d, qmax, g_bf16;
+  int T, d, qmax, g_bf16;
   void* H;             // x + r in x's type, or nullptr
   void* Y;             // normed row in x's type, or nullptr
   uint8_t* codes;
@@ -54,118 +52,182 @@ __device__ __forceinline__ void st8(void* p, size_t i, bool bf16, const float (&
   }
 }
 
-// One CTA per row. A thread holds VPT vectors of eight neighbouring channels, blockDim.x vectors apart,
-// in registers from the only read of the row to the last write.
+// Eight elements as loaded: their use is far from their load.
+template <bool BF16>
+struct Raw8 {
+  uint4 v[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ void ld_raw(const void* p, size_t i, Raw8<BF16>& r) {
+  if constexpr (BF16) {
+    r.v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  } else {
+    r.v[0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i)[0];
+    r.v[1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i)[1];
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Raw8<BF16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(w[i]);
+      v[4 + i] = __uint_as_float(u[i]);
+    }
+  }
+}
+// v[i] = fl32(x[i] + v[i])
+template <bool BF16>
+__device__ __forceinline__ void add_raw(const Raw8<BF16>& x, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // the bf16 operand is widened in the addition itself
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+          : "+f"(v[2 * i]), "+f"(v[2 * i + 1])
+          : "r"(w[i]));
+  } else {
+    float f[8];
+    unpack<false>(x, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(f[i], v[i]);
+  }
+}
+
+// The row statistic from the warps' sums of squares (one warp): held in 64 bits and rounded once.
+__device__ __forceinline__ void norm_rstd(const double* sum_s, int nw, int lane, const NormArgs& a, float* rstd) {
+  double sum = lane < nw ? sum_s[lane] : 0.0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) *rstd = static_cast<float>(rsqrt(sum / a.d + a.eps));
+}
+
+// A thread holds VPT vectors of eight neighbouring channels of a row, blockDim.x vectors apart, in registers
+// from the row's only read to its last write.
 //   h = fl32(x + r); rstd = fl32(1/sqrt(sum h^2 / d + eps)); y = fl32(fl32(h*rstd)*g); v = fl32(y*s_inv)
 // The sum of squares is held in 64 bits and rstd rounded once, after which every value that decides a
 // code is one fp32 operation, so the codes do not depend on the order of the sum.
-template <bool BF16, int VPT, int MAXT, int OUT>
-__global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const NormArgs a) {
+// HBM bound: 8192 x 8192 bf16 with residual, A6: 104 us, 5.8 TB/s; MXFP4: 93 us, 6.1 TB/s. Persistent CTAs that load
+// a row ahead, and several rows to a CTA, were slower (117-136 and 125 us for A6): the registers they take cost
+// more resident warps than they save waits.
+template <bool BF16, int VPT, int OUT>
+__global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
   __shared__ double sum_s[32];
   __shared__ uint32_t top_s[32];
   __shared__ float rstd_s;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  const size_t row = blockIdx.x, base = row * a.d;
+  const int KT = (a.d + kMxTileCols - 1) / kMxTileCols;
+  Raw8<BF16> x[VPT], q[VPT];
   float h[VPT][8];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int k = (tid + j * nt) * 8;
-    if (k < a.d) {
-      ld8(a.X, base + k, BF16, h[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-    }
-  }
-  if (a.R) {
-    float r[VPT][8];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int k = (tid + j * nt) * 8;
-      if (k < a.d) ld8(a.R, base + k, BF16, r[j]);
-    }
+  auto load = [&](size_t row) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int k = (tid + j * nt) * 8;
       if (k < a.d) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], r[j][i]);
-        if (a.H) st8(a.H, base + k, BF16, h[j]);
+        ld_raw<BF16>(a.X, row * a.d + k, x[j]);
+        if (a.R) ld_raw<BF16>(a.R, row * a.d + k, q[j]);
       }
     }
-  }
-  double sum = 0.0;
+  };
+  // h of a row, its copy to H, and this warp's sum of squares
+  auto add = [&](size_t row) {
+    double sum = 0.0;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      if (k < a.d) {
+        if (a.R) {
+          unpack<BF16>(q[j], h[j]);
+          add_raw<BF16>(x[j], h[j]);
+          if (a.H) st8(a.H, row * a.d + k, BF16, h[j]);
+        } else {
+          unpack<BF16>(x[j], h[j]);
+        }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[j][i]), static_cast<double>(h[j][i]), sum);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  if (warp == 0) {
-    sum = lane < nw ? sum_s[lane] : 0.0;
+        for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[j][i]), static_cast<double>(h[j][i]), sum);
+      }
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) rstd_s = static_cast<float>(1.0 / sqrt(sum / a.d + a.eps));
-  }
-  __syncthreads();
-  const float rstd = rstd_s;
-  uint32_t top = 0;
+    if (lane == 0) sum_s[warp] = sum;
+  };
+  // y and v of a row, and this warp's largest |v|: magnitudes order as unsigned bit patterns, with infinities
+  // and NaNs above every finite value
+  auto scale = [&](size_t row) {
+    const float rstd = rstd_s;
+    uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int k = (tid + j * nt) * 8;
-    if (k < a.d) {
-      float g[8];
-      ld8(a.gamma, k, a.g_bf16, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(__fmul_rn(h[j][i], rstd), g[i]);
-      if (a.Y) st8(a.Y, base + k, BF16, h[j]);
-      if (OUT != kOutNone && a.s_inv) {
-        float s[8];
-        ld8(a.s_inv, k, false, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(h[j][i], s[i]);
+    for (int j = 0; j < VPT; ++j) {
+      const int k = (tid + j * nt) * 8;
+      if (k < a.d) {
+        float g[8];
+        ld8(a.gamma, k, a.g_bf16, g);
+        mul8(h[j], rstd);
+        mul8(h[j], g);
+        if (a.Y) st8(a.Y, row * a.d + k, BF16, h[j]);
+        if (OUT != kOutNone && a.s_inv) {
+          ld8(a.s_inv, k, false, g);
+          mul8(h[j], g);
+        }
+        if (OUT == kOutInt8) top = max(top, absmax8(h[j]));
       }
-      if (OUT == kOutInt8) top = max(top, absmax8(h[j]));
     }
-  }
-  if (OUT == kOutInt8) {
-    // magnitudes order as unsigned bit patterns, with infinities and NaNs above every finite value
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) top_s[warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < nw ? top_s[lane] : 0u);
+    if (OUT == kOutInt8) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) top_s[warp] = top;
+    }
+    if (OUT == kOutMx4) {
+      // four neighbouring lanes hold a block (rows are whole blocks); the first writes its scale
+      uint8_t* sc = static_cast<uint8_t*>(a.scales) + mx_scale_row(row, KT);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int k = (tid + j * nt) * 8;
+        uint32_t t = k < a.d ? absmax8(h[j]) : 0u;
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        const uint32_t byte = mx_scale_byte(t);
+        if (k < a.d) *reinterpret_cast<uint32_t*>(a.codes + (row * a.d + k) / 2) = mx_codes8(h[j], byte);
+        if ((lane & 3) == 0 && k < KT * kMxTileCols) sc[mx_scale_at(k)] = static_cast<uint8_t>(k < a.d ? byte : kMxOne);
+      }
+    }
+  };
+  // the int8 codes of a row
+  auto codes = [&](size_t row) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, lane < nw ? top_s[lane] : 0u);
     const bool finite = top < 0x7F800000u;
     const float sa = finite ? __fdiv_rn(__uint_as_float(top), static_cast<float>(a.qmax)) : __uint_as_float(0x7FC00000u);
     if (tid == 0) static_cast<float*>(a.scales)[row] = sa;
     const float inv = sa > 0.0f ? __frcp_rn(sa) : 0.0f;
-    const bool fast = rtn_fast_ok(sa, inv);
+    const float limit = rtn_fast_ok(sa, inv) ? rtn_limit(a.qmax) : 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int k = (tid + j * nt) * 8;
       if (k < a.d) {
         uint32_t w0 = 0, w1 = 0;
-        if (finite) rtn_code8_row(h[j], sa, inv, fast, a.qmax, w0, w1);
-        *reinterpret_cast<uint2*>(a.codes + base + k) = make_uint2(w0, w1);
+        if (finite) rtn_code8_row(h[j], sa, inv, limit, a.qmax, w0, w1);
+        *reinterpret_cast<uint2*>(a.codes + row * a.d + k) = make_uint2(w0, w1);
       }
     }
-  }
-  if (OUT == kOutMx4) {
-    // four neighbouring lanes hold a block (rows are whole blocks); the first writes its scale
-    const int KT = (a.d + kMxTileCols - 1) / kMxTileCols;
-    uint8_t* sc = static_cast<uint8_t*>(a.scales) + mx_scale_row(row, KT);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int k = (tid + j * nt) * 8;
-      uint32_t t = k < a.d ? absmax8(h[j]) : 0u;
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      const uint32_t byte = mx_scale_byte(t);
-      if (k < a.d) *reinterpret_cast<uint32_t*>(a.codes + (base + k) / 2) = mx_codes8(h[j], byte);
-      if ((lane & 3) == 0 && k < KT * kMxTileCols) sc[mx_scale_at(k)] = static_cast<uint8_t>(k < a.d ? byte : kMxOne);
-    }
+  };
+
+  const size_t row = blockIdx.x;
+  load(row);
+  add(row);
+  __syncthreads();
+  if (warp == 0) norm_rstd(sum_s, nw, lane, a, &rstd_s);
+  __syncthreads();
+  scale(row);
+  if (OUT == kOutInt8) {
+    __syncthreads();
+    codes(row);
   }
 }
 
@@ -198,23 +260,28 @@ __global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ 
   }
 }
 
-template <bool BF16, int VPT, int MAXT>
-cudaError_t launch_norm_t(const NormArgs& a, int out, int T, cudaStream_t st) {
+template <bool BF16, int VPT>
+cudaError_t launch_norm_t(const NormArgs& a, int out, cudaStream_t st) {
   const int threads = static_cast<int>(round_up(ceil_div(a.d / 8, VPT), 32));
-  if (threads > MAXT) return cudaErrorInvalidConfiguration;
-  if (out == kOutInt8) k_add_rmsnorm<BF16, VPT, MAXT, kOutInt8><<<T, threads, 0, st>>>(a);
-  else if (out == kOutMx4) k_add_rmsnorm<BF16, VPT, MAXT, kOutMx4><<<T, threads, 0, st>>>(a);
-  else k_add_rmsnorm<BF16, VPT, MAXT, kOutNone><<<T, threads, 0, st>>>(a);
+  auto k = out == kOutInt8 ? k_add_rmsnorm<BF16, VPT, kOutInt8>
+           : out == kOutMx4 ? k_add_rmsnorm<BF16, VPT, kOutMx4>
+                            : k_add_rmsnorm<BF16, VPT, kOutNone>;
+  k<<<a.T, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
+// Vectors per thread. With at most two rows per SM latency counts, and a row takes as many threads as it has
+// vectors, up to 1024 (300 x 4096 int8: 5.4 us against 6.0 with two). With more rows, fewer and fatter warps pay
+// less for the block reductions and keep as many bytes in flight (8192 x 8192 bf16 A6: 201 us with one vector,
+// 127 with two, 104 with four, 118 with eight at half the warps; 4096 x 4096: 38, 31, 32); fp32 rows have twice
+// the bytes for the same work and stop at two (4096 x 8192: 98 us, and 110 with four).
 template <bool BF16>
-cudaError_t launch_norm_x(const NormArgs& a, int out, int T, cudaStream_t st) {
+cudaError_t launch_norm_x(const NormArgs& a, int out, cudaStream_t st) {
   const int vecs = a.d / 8;
-  if (vecs <= 256) return launch_norm_t<BF16, 1, 1024>(a, out, T, st);
-  if (vecs <= 512) return launch_norm_t<BF16, 2, 1024>(a, out, T, st);
-  if (vecs <= 1024) return launch_norm_t<BF16, 4, 256>(a, out, T, st);
-  return launch_norm_t<BF16, 4, 1024>(a, out, T, st);
+  const bool few = a.T <= 2 * decode_grid_sms();
+  if (vecs <= (few ? 1024 : 256)) return launch_norm_t<BF16, 1>(a, out, st);
+  if (vecs <= (few ? 2048 : BF16 ? 512 : 1024)) return launch_norm_t<BF16, 2>(a, out, st);
+  return launch_norm_t<BF16, 4>(a, out, st);
 }
 
 }  // namespace
@@ -229,6 +296,7 @@ cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const 
   a.gamma = gamma;
   a.s_inv = s_inv;
   a.eps = eps;
+  a.T = T;
   a.d = d;
   a.qmax = (1 << (a_bits - 1)) - 1;
   a.g_bf16 = g_bf16;
@@ -237,7 +305,7 @@ cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const 
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
   const int out = a_bits == 16 ? kOutNone : a_bits == 4 ? kOutMx4 : kOutInt8;
-  return x_bf16 ? launch_norm_x<true>(a, out, T, st) : launch_norm_x<false>(a, out, T, st);
+  return x_bf16 ? launch_norm_x<true>(a, out, st) : launch_norm_x<false>(a, out, st);
 }
 
 cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int d, void* out, bool out_bf16,

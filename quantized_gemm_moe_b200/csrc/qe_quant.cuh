@@ -134,31 +134,53 @@ __device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
   return __float_as_uint(max3_abs(m, v[7], v[7]));
 }
 
+// a[i] * b[i], a[i] * x and a[i] + x, two per instruction (each one IEEE operation).
+__device__ __forceinline__ void mul8(float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a[i]), "+f"(a[i + 1])
+        : "f"(b[i]), "f"(b[i + 1]));
+}
+__device__ __forceinline__ void mul8(float (&a)[8], float x) {
+  const float b[8] = {x, x, x, x, x, x, x, x};
+  mul8(a, b);
+}
+
 // Codes of eight values of a block whose scale byte is `byte`. v * 2^-E is exact unless it falls below
 // fp32's normal range, where the code is 0 either way.
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
-  const float inv = mx_inv_scale(byte);
-  float a[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = v[i] * inv;
-  return byte == 255u ? 0u : e2m1_pack8(a);
+  float a[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+  mul8(a, mx_inv_scale(byte));
+  const uint32_t code = e2m1_pack8(a);
+  return byte == 255u ? 0u : code;
 }
 
-// rtn_code8 for a row whose scale came from its own finite absmax, so that |v * inv| <= qmax (1 + 2^-22) and the
-// clamp cannot bind.
-__device__ __forceinline__ void rtn_code8_row(const float (&v)[8], float scale, float inv, bool fast, int qmax,
+// rtn_code8 for a row whose scale came from its own finite absmax, so that g = fl32(v * inv) has |g| <= qmax (1 + 2^-22)
+// and the clamp cannot bind. g is off the correctly rounded quotient by at most 3 * 2^-24 |g|, below
+// (qmax + 1) * 2^-22, so rint(g) is the code when its distance to g stays below limit = 0.5 - (qmax + 1) * 2^-22.
+__device__ __forceinline__ float rtn_limit(int qmax) {
+  return 0.5f - static_cast<float>(qmax + 1) * 2.384185791015625e-07f;
+}
+__device__ __forceinline__ void rtn_code8_row(const float (&v)[8], float scale, float inv, float limit, int qmax,
                                               uint32_t& w0, uint32_t& w1) {
-  constexpr float kM = 12582912.0f;
   uint32_t b[8];
   float d[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float g = __fmul_rn(v[i], inv);
-    const float t = __fadd_rn(g, kM);
-    d[i] = __fmaf_rn(fabsf(g), 9.5367431640625e-07f, fabsf(__fsub_rn(g, __fsub_rn(t, kM))));
-    b[i] = __float_as_uint(t);
+  for (int i = 0; i < 8; i += 2) {
+    float t0, t1;
+    asm("{\n\t.reg .b64 g, t, r, k;\n\t"
+        "mov.b64 g, {%4, %5};\n\tmov.b64 k, {%6, %6};\n\tmul.rn.f32x2 g, g, k;\n\t"
+        "mov.b64 k, {0f4B400000, 0f4B400000};\n\tadd.rn.f32x2 t, g, k;\n\t"
+        "mov.b64 k, {0fCB400000, 0fCB400000};\n\tadd.rn.f32x2 r, t, k;\n\t"
+        "mov.b64 k, {0fBF800000, 0fBF800000};\n\tfma.rn.f32x2 g, r, k, g;\n\t"
+        "mov.b64 {%0, %1}, t;\n\tmov.b64 {%2, %3}, g;\n\t}"
+        : "=f"(t0), "=f"(t1), "=f"(d[i]), "=f"(d[i + 1])
+        : "f"(v[i]), "f"(v[i + 1]), "f"(inv));
+    b[i] = __float_as_uint(t0);
+    b[i + 1] = __float_as_uint(t1);
   }
-  if (fast && absmax8(d) < 0x3F000000u) {  // every distance to rint(g), with its margin, below 0.5
+  if (absmax8(d) < __float_as_uint(limit)) {
     w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
     return;
@@ -168,28 +190,6 @@ __device__ __forceinline__ void rtn_code8_row(const float (&v)[8], float scale, 
   w1 = w.y;
 }
 
-// 32 bytes at p: one load where p is 32-byte aligned, else two.
-__device__ __forceinline__ void ldg_32b(const void* p, bool aligned32, uint32_t (&w)[8]) {
-  if (aligned32) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-}
-__device__ __forceinline__ void stg_32b(void* p, bool aligned32, const uint32_t (&w)[8]) {
-  if (aligned32) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 // Two fp32 values as a word of bf16 (the first in the low half).
 __device__ __forceinline__ uint32_t bf16x2_word(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
