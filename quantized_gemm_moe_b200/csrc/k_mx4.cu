@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const void* __re
                                                                 int rows, int cols, int spans, size_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
+  grid_dep_launch();  // a product may set itself up, and load its weights, meanwhile
   const int lane = threadIdx.x & 31;
   const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;

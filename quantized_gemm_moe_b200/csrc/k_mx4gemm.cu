@@ -9,54 +9,88 @@ namespace qe {
 namespace {
 
 constexpr int kMxStageK = 256;  // channels per pipeline stage: 128 bytes of codes, one swizzle row
-constexpr int kSplitThreads = 192;
-
-struct MxArgs {
+// ------------------------------------------------------------------ few tokens
+struct SplitArgs {
   const uint8_t* w_scales;
   const uint8_t* x_scales;
-  int T, N, K, KT;  // KT = ceil(K / 128) scale tiles along K
+  int T, N, K, KT;      // KT = ceil(K / 128) scale tiles along K
+  int bn, nb, splits;   // tokens per tile (a multiple of 16), scale tiles across them, CTAs along K
+  int stages, tmem_cols;
+  int w_early;          // the weights were written before the previous kernel began
   void* Y;
   int y_bf16;
   int* err;
 };
+constexpr int kSplitThreads = 192;
+constexpr int kSplitA = 16384, kSplitSA = 1024;
 
-template <int BN>
-struct SplitCfg {
-  static constexpr int kNB = (BN + 127) / 128;  // scale tiles across the token tile
-  static constexpr int kA = 16384, kB = BN * 128, kSA = 1024, kSB = 1024 * kNB;
-  static constexpr int kStage = kA + kB + kSA + kSB;
-  static constexpr int kStages = BN <= 16 ? 5 : BN <= 64 ? 4 : BN <= 128 ? 3 : 4;
-  static constexpr int kSfCols = 8 + 8 * kNB;   // tensor memory columns of a stage's scales
-  static constexpr int kTmemUsed = BN + 2 * kSfCols;
-  static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
-  static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
-  static_assert(BN * 128 * 4 <= kStages * kStage, "the partial tile reuses the stages");
-};
+__host__ __device__ constexpr int split_stage_bytes(int bn) { return kSplitA + bn * 128 + kSplitSA + 1024 * ((bn + 127) / 128); }
+__host__ __device__ constexpr int split_sf_cols(int nb) { return 8 + 8 * nb; }  // tensor memory columns of a stage's scales
+// Room for two CTAs on an SM up to 128 tokens, and for one above.
+constexpr int split_stages(int bn) { return (bn <= 128 ? 114176 : 230912) / split_stage_bytes(bn); }
 
-// Y tile of 128 output channels (MMA rows) x BN tokens (MMA columns), the K range split over the cluster's
+// Adds the cluster's partial tiles in rank order, four channels of a token at a time, and writes this CTA's
+// share of them.
+template <int S>
+__device__ __forceinline__ void split_reduce(const SplitArgs& a, uint32_t part, int rank, int n0, int t0, int ncols) {
+  uint32_t from[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) from[r] = S > 1 ? mapa(part, r) : part;
+  const int total = ncols * 32;
+  const int i1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / S);
+  for (int i = static_cast<int>(static_cast<int64_t>(total) * rank / S) + threadIdx.x; i < i1; i += kSplitThreads) {
+    float4 p[S];
+#pragma unroll
+    for (int r = 0; r < S; ++r) p[r] = ld_cluster_f32x4(from[r] + i * 16);
+    float4 v = p[0];
+#pragma unroll
+    for (int r = 1; r < S; ++r) {
+      v.x += p[r].x;
+      v.y += p[r].y;
+      v.z += p[r].z;
+      v.w += p[r].w;
+    }
+    const int n = n0 + (i & 31) * 4;
+    const size_t y = static_cast<size_t>(t0 + (i >> 5)) * a.N + n;
+    if ((a.N & 3) == 0) {
+      if (n < a.N) {
+        if (a.y_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.Y) + y) = make_uint2(bf16x2_word(v.x, v.y), bf16x2_word(v.z, v.w));
+        else *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + y) = v;
+      }
+    } else {
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (n + j < a.N) {
+          if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y + j] = f32_to_bf16_bits(f[j]);
+          else static_cast<float*>(a.Y)[y + j] = f[j];
+        }
+      }
+    }
+  }
+}
+
+// Y tile of 128 output channels (MMA rows) x bn tokens (MMA columns), the K range split over the cluster's
 // CTAs, whose fp32 partial tiles are then added in rank order through distributed shared memory.
 // Weights stream once through each CTA's ring of TMA stages, so few tokens are bound by HBM; clusters make
 // enough CTAs to keep all SMs streaming when there are few tiles.
-template <int BN>
 __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_constant__ CUtensorMap tm_w,
-                                                             const __grid_constant__ CUtensorMap tm_x, const MxArgs a,
-                                                             int splits) {
-  using C = SplitCfg<BN>;
-  constexpr int NS = C::kStages;
+                                                             const __grid_constant__ CUtensorMap tm_x,
+                                                             const SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * C::kStage);
+  const int NS = a.stages, kB = a.bn * 128, stage = split_stage_bytes(a.bn), sf_cols = split_sf_cols(a.nb);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * stage);
   uint64_t* empty = full + NS;
   uint64_t* accf = empty + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int n_tile = blockIdx.x / splits, n0 = n_tile * 128, t0 = blockIdx.y * BN;
+  const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int n_tile = blockIdx.x / a.splits, n0 = n_tile * 128, t0 = blockIdx.y * a.bn;
   const int KS = (a.K + kMxStageK - 1) / kMxStageK;
-  const int s0 = static_cast<int>(static_cast<int64_t>(KS) * rank / splits);
-  const int nk = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / splits) - s0;
-  const int ncols = min(BN, a.T - t0);
+  const int s0 = static_cast<int>(static_cast<int64_t>(KS) * rank / a.splits);
+  const int nk = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / a.splits) - s0;
+  const int ncols = min(a.bn, a.T - t0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -69,62 +103,74 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
     prefetch_tmap(&tm_x);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_alloc(tmem_slot, a.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  bool acc_ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
-      for (; it < nk; ++it) {
+      // scale tiles of the token tile: the first may start inside a 128-row tile only when it is the only one
+      const size_t rb = t0 / 128;
+      const int nb = min(a.nb, static_cast<int>((a.T + 127) / 128 - rb));
+      auto load_w = [&](int it) {
         const int s = it % NS, ks = s0 + it;
-        if (!mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, a.err, DEVERR_WAIT_PRODUCER)) break;
-        uint8_t* st = smem + s * C::kStage;
+        uint8_t* st = smem + s * stage;
         const uint32_t sf = kMxTileBytes * min(2, a.KT - 2 * ks);
-        const size_t rb = t0 / 128;
-        const bool two = C::kNB == 2 && t0 + 128 < a.T;
-        mbar_arrive_expect_tx(&full[s], C::kA + C::kB + sf * (two ? 3 : 2));
+        mbar_arrive_expect_tx(&full[s], kSplitA + kB + sf * (1 + nb));
         tma_load_2d(st, &tm_w, ks * 128, n0, &full[s]);
-        tma_load_2d(st + C::kA, &tm_x, ks * 128, t0, &full[s]);
-        bulk_load(st + C::kA + C::kB, a.w_scales + (static_cast<size_t>(n_tile) * a.KT + 2 * ks) * kMxTileBytes, sf,
-                  &full[s]);
-        bulk_load(st + C::kA + C::kB + C::kSA, a.x_scales + (rb * a.KT + 2 * ks) * kMxTileBytes, sf, &full[s]);
-        if (two)
-          bulk_load(st + C::kA + C::kB + C::kSA + 1024, a.x_scales + ((rb + 1) * a.KT + 2 * ks) * kMxTileBytes, sf,
-                    &full[s]);
+        bulk_load(st + kSplitA + kB, a.w_scales + (static_cast<size_t>(n_tile) * a.KT + 2 * ks) * kMxTileBytes, sf, &full[s]);
+      };
+      auto load_x = [&](int it) {
+        const int s = it % NS, ks = s0 + it;
+        uint8_t* st = smem + s * stage;
+        const uint32_t sf = kMxTileBytes * min(2, a.KT - 2 * ks);
+        tma_load_2d(st + kSplitA, &tm_x, ks * 128, t0, &full[s]);
+        for (int b = 0; b < nb; ++b)
+          bulk_load(st + kSplitA + kB + kSplitSA + 1024 * b, a.x_scales + ((rb + b) * a.KT + 2 * ks) * kMxTileBytes, sf, &full[s]);
+      };
+      const int ahead = min(nk, NS);
+      if (!a.w_early) grid_dep_wait();
+      for (int it = 0; it < ahead; ++it) load_w(it);
+      if (a.w_early) grid_dep_wait();
+      for (int it = 0; it < ahead; ++it) load_x(it);
+      int it = ahead;
+      for (; it < nk; ++it) {
+        if (!mbar_wait(&empty[it % NS], ((it / NS) & 1) ^ 1, a.err, DEVERR_WAIT_PRODUCER)) break;
+        load_w(it);
+        load_x(it);
       }
       drain_ring(full, NS, it);
     }
     __syncwarp();
   } else if (warp == 1) {
-    constexpr uint32_t id = idesc_mxf4(128, BN);
+    const uint32_t id = idesc_mxf4(128, a.bn);
     const bool leader = elect_one();
     for (int it = 0; it < nk; ++it) {
       const int s = it % NS, ks = s0 + it;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (it / NS) & 1, a.err, DEVERR_WAIT_MMA))) break;
       tc_fence_after();
       if (leader) {
-        const uint32_t at = smem_u32(smem + s * C::kStage);
-        const uint32_t sfa = tmem + BN + (it & 1) * C::kSfCols, sfb = sfa + 8;
+        const uint32_t at = smem_u32(smem + s * stage);
+        const uint32_t sfa = tmem + a.bn + (it & 1) * sf_cols, sfb = sfa + 8;
         const int tiles = min(2, a.KT - 2 * ks);
-        const uint32_t sa = at + C::kA + C::kB, sb = sa + C::kSA;
+        const uint32_t sa = at + kSplitA + kB, sb = sa + kSplitSA;
         for (int k = 0; k < tiles; ++k) {
           tmem_cp_32x128b(sfa + 4 * k, smem_desc_rows16(sa + k * kMxTileBytes));
-#pragma unroll
-          for (int b = 0; b < C::kNB; ++b)
-            tmem_cp_32x128b(sfb + (k * C::kNB + b) * 4, smem_desc_rows16(sb + b * 1024 + k * kMxTileBytes));
+          for (int b = 0; b < a.nb; ++b)
+            tmem_cp_32x128b(sfb + (k * a.nb + b) * 4, smem_desc_rows16(sb + b * 1024 + k * kMxTileBytes));
         }
-        const uint64_t da = smem_desc_sw128(at), db = smem_desc_sw128(at + C::kA);
+        const uint64_t da = smem_desc_sw128(at), db = smem_desc_sw128(at + kSplitA);
         const int mmas = min(4, (a.K - ks * kMxStageK + 63) / 64);
-        for (int m = 0; m < mmas; ++m) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
           const uint32_t sel = static_cast<uint32_t>(m & 1) * 2;
-          mma_mxf4(tmem, da + 2 * m, db + 2 * m, id | (sel << 29) | (sel << 4), sfa + 4 * (m >> 1),
-                   sfb + 4 * C::kNB * (m >> 1), (it | m) != 0);
+          if (m < mmas)
+            mma_mxf4(tmem, da + 2 * m, db + 2 * m, id | (sel << 29) | (sel << 4), sfa + 4 * (m >> 1),
+                     sfb + 4 * a.nb * (m >> 1), (it | m) != 0);
         }
         tc_commit(&empty[s]);
         if (it == nk - 1) tc_commit(accf);
@@ -132,54 +178,34 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
       __syncwarp();
     }
   } else {
-    acc_ok = mbar_wait(accf, 0, a.err, DEVERR_WAIT_EPILOGUE);
-    acc_ok = __all_sync(0xffffffffu, acc_ok);
-    tc_fence_after();
-    const int q = warp & 3;
-    const int o = 32 * q + lane;
+    // the partial tile [token][channel], over the stages: all of them have been read
+    const int o = 32 * (warp & 3) + lane;
     float* part = reinterpret_cast<float*>(smem);
-    if (acc_ok) {
+    if (__all_sync(0xffffffffu, mbar_wait(accf, 0, a.err, DEVERR_WAIT_EPILOGUE))) {
+      tc_fence_after();
       for (int c0 = 0; c0 < ncols; c0 += 16) {
         uint32_t v[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + c0, v);
+        tmem_ld16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c0, v);
         tmem_wait_ld();
         reg_fence(v);
-        if (splits > 1) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + o] = __uint_as_float(v[j]);
-        } else if (n0 + o < a.N) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c0 + j < ncols) {
-              const size_t y = static_cast<size_t>(t0 + c0 + j) * a.N + n0 + o;
-              if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(__uint_as_float(v[j]));
-              else static_cast<float*>(a.Y)[y] = __uint_as_float(v[j]);
-            }
-          }
-        }
+        for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + o] = __uint_as_float(v[j]);
       }
     }
     tc_fence_before();
   }
-  if (splits > 1) {
-    cluster_sync_all();
-    const uint32_t part = smem_u32(smem);
-    const int total = ncols * 128;
-    const int i1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / splits);
-    for (int i = static_cast<int>(static_cast<int64_t>(total) * rank / splits) + threadIdx.x; i < i1; i += kSplitThreads) {
-      float v = 0.0f;
-      for (int r = 0; r < splits; ++r) v += ld_cluster_f32(mapa(part + i * 4, r));
-      const int n = n0 + (i & 127);
-      if (n < a.N) {
-        const size_t y = static_cast<size_t>(t0 + (i >> 7)) * a.N + n;
-        if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(v);
-        else static_cast<float*>(a.Y)[y] = v;
-      }
-    }
-    cluster_sync_all();  // no CTA leaves while another may still read its partial tile
+  if (a.splits > 1) cluster_sync_all();
+  else __syncthreads();
+  const uint32_t part = smem_u32(smem);
+  switch (a.splits) {
+    case 1: split_reduce<1>(a, part, rank, n0, t0, ncols); break;
+    case 2: split_reduce<2>(a, part, rank, n0, t0, ncols); break;
+    case 4: split_reduce<4>(a, part, rank, n0, t0, ncols); break;
+    default: split_reduce<8>(a, part, rank, n0, t0, ncols); break;
   }
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (a.splits > 1) cluster_sync_all();  // no CTA leaves while another may still read its partial tile
+  else __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -207,10 +233,11 @@ struct PairCfg {
 constexpr int kPairThreads = 64 + 32 * PairCfg::kEpiWarps;
 
 struct PairArgs {
-  int T, N, K, KT;
+  int T, N, K;
   int m_tiles, n_tiles, group;  // group: token tiles walked together, so that their activations stay in L2
   void* Y;
   int y_bf16, tma;              // tma: Y's rows are multiples of 16 bytes
+  int w_early;                  // the weights were written before the previous kernel began
   int* err;
 };
 
@@ -285,7 +312,7 @@ __device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap*
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+__global__ void __launch_bounds__(kPairThreads)
     k_mx4_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                const __grid_constant__ CUtensorMap tm_y, const PairArgs a) {
@@ -332,26 +359,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
+      // stage it of tile (mt, nt); the even CTA's barrier counts both CTAs' bytes
+      auto load_w = [&](int it, int ks, int nt) {
+        const int s = it % NS;
+        uint8_t* st = smem + s * C::kStage;
+        if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+        const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+        tma_load_2d_pair(st + C::kA, &tm_w, ks * 128, nt * 256 + cta * 128, bar);
+        tma_load_2d_pair(st + C::kA + C::kB + C::kSA, &tm_ws, ks * 256, nt * 2, bar);
+      };
+      auto load_x = [&](int it, int ks, int mt) {
+        const int s = it % NS;
+        uint8_t* st = smem + s * C::kStage;
+        const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+        tma_load_2d_pair(st, &tm_x, ks * 128, mt * 256 + cta * 128, bar);
+        tma_load_2d_pair(st + C::kA + C::kB, &tm_xs, ks * 256, mt * 2 + cta, bar);
+      };
+      int it = 0, ahead = min(KS, NS);
       bool ok = true;
+      if (!a.w_early) grid_dep_wait();
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
         int mt, nt;
         pair_tile(a, tile, mt, nt);
-        const int m0 = mt * 256 + cta * 128, n0 = nt * 256 + cta * 128;
-        for (int ks = 0; ks < KS; ++ks, ++it) {
-          const int s = it % NS;
-          if (!mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, a.err, DEVERR_WAIT_PRODUCER)) {
+        int ks = 0;
+        if (it == 0) {  // the first stages are free, and their weights need no wait
+          for (ks = 0; ks < ahead; ++ks) load_w(ks, ks, nt);
+          if (a.w_early) grid_dep_wait();
+          for (ks = 0; ks < ahead; ++ks) load_x(ks, ks, mt);
+          it = ahead;
+        }
+        for (; ks < KS; ++ks, ++it) {
+          if (!mbar_wait(&empty[it % NS], ((it / NS) & 1) ^ 1, a.err, DEVERR_WAIT_PRODUCER)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * C::kStage;
-          // the even CTA's barrier counts both CTAs' bytes
-          if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
-          const uint32_t bar = mapa(smem_u32(&full[s]), 0);
-          tma_load_2d_pair(st, &tm_x, ks * 128, m0, bar);
-          tma_load_2d_pair(st + C::kA, &tm_w, ks * 128, n0, bar);
-          tma_load_2d_pair(st + C::kA + C::kB, &tm_xs, ks * 256, mt * 2 + cta, bar);
-          tma_load_2d_pair(st + C::kA + C::kB + C::kSA, &tm_ws, ks * 256, nt * 2, bar);
+          load_w(it, ks, nt);
+          load_x(it, ks, mt);
         }
       }
       if (cta == 0) drain_ring(full, NS, it);
@@ -439,26 +482,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int BN>
-cudaError_t launch_split_t(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const MxArgs& a, const Mx4Plan& p,
-                           cudaStream_t st) {
-  using C = SplitCfg<BN>;
-  cudaError_t e = cudaFuncSetAttribute(k_mx4_split<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(C::kSmem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles * p.splits), static_cast<unsigned>(p.t_tiles));
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+cudaError_t launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned gx, unsigned gy, int threads,
+                       size_t smem, int cluster, cudaStream_t st) {
+  cfg.gridDim = dim3(gx, gy);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_mx4_split<BN>, tm_w, tm_x, a, p.splits);
+  cfg.numAttrs = 2;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -476,11 +514,12 @@ Mx4Plan plan_mx4(int T, int N, int K) {
     p.ctas = static_cast<int>(2 * std::min<int64_t>(sms / 2, static_cast<int64_t>(p.n_tiles) * p.t_tiles));
     return p;
   }
-  p.bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  p.t_tiles = static_cast<int>(ceil_div(T, 256));
+  // several token tiles start on whole scale tiles
+  p.bn = p.t_tiles == 1 ? static_cast<int>(round_up(T, 16)) : 256;
   p.n_tiles = static_cast<int>(ceil_div(N, 128));
-  p.t_tiles = static_cast<int>(ceil_div(T, p.bn));
-  // as many CTAs as two per SM (one at 256 tokens) hold, in clusters of at most eight along K
-  const int slots = p.bn == 256 ? sms : 2 * sms;
+  // as many CTAs as two per SM (one above 128 tokens) hold, in clusters of at most eight along K
+  const int slots = p.bn > 128 ? sms : 2 * sms;
   const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.t_tiles;
   const int stages = static_cast<int>(ceil_div(K, kMxStageK));
   p.splits = 1;
@@ -491,7 +530,7 @@ Mx4Plan plan_mx4(int T, int N, int K) {
 
 cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const CUtensorMap& tm_ws,
                             const CUtensorMap& tm_xs, const CUtensorMap* tm_y, const Mx4Plan& p, int T, int N, int K,
-                            void* Y, bool y_bf16, int* err, cudaStream_t st) {
+                            void* Y, bool y_bf16, bool w_early, int* err, cudaStream_t st) {
   using C = PairCfg;
   cudaError_t e = cudaFuncSetAttribute(k_mx4_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
@@ -499,38 +538,48 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
   a.T = T;
   a.N = N;
   a.K = K;
-  a.KT = static_cast<int>(ceil_div(K, kMxTileCols));
   a.m_tiles = p.t_tiles;
   a.n_tiles = p.n_tiles;
   a.group = std::min(p.t_tiles, 8);
   a.Y = Y;
   a.y_bf16 = y_bf16;
   a.tma = tm_y != nullptr;
+  a.w_early = w_early;
   a.err = err;
-  k_mx4_pair<<<p.ctas, kPairThreads, C::kSmem, st>>>(tm_x, tm_w, tm_xs, tm_ws, tm_y ? *tm_y : tm_x, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  launch_cfg(cfg, attr, p.ctas, 1, kPairThreads, C::kSmem, 2, st);
+  return cudaLaunchKernelEx(&cfg, k_mx4_pair, tm_x, tm_w, tm_xs, tm_ws, tm_y ? *tm_y : tm_x, a);
 }
 
-cudaError_t launch_mx4_product(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
-                               const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, int* err,
-                               cudaStream_t st) {
-  MxArgs a{};
+cudaError_t launch_mx4_split(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
+                             const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, bool w_early, int* err,
+                             cudaStream_t st) {
+  SplitArgs a{};
   a.w_scales = w_scales;
   a.x_scales = x_scales;
   a.T = T;
   a.N = N;
   a.K = K;
   a.KT = static_cast<int>(ceil_div(K, kMxTileCols));
+  a.bn = p.bn;
+  a.nb = static_cast<int>(ceil_div(p.bn, 128));
+  a.splits = p.splits;
+  a.stages = split_stages(p.bn);
+  const int cols = p.bn + 2 * split_sf_cols(a.nb);
+  a.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  a.w_early = w_early;
   a.Y = Y;
   a.y_bf16 = y_bf16;
   a.err = err;
-  switch (p.bn) {
-    case 16: return launch_split_t<16>(tm_w, tm_x, a, p, st);
-    case 32: return launch_split_t<32>(tm_w, tm_x, a, p, st);
-    case 64: return launch_split_t<64>(tm_w, tm_x, a, p, st);
-    case 128: return launch_split_t<128>(tm_w, tm_x, a, p, st);
-    default: return launch_split_t<256>(tm_w, tm_x, a, p, st);
-  }
+  const size_t smem = 1024 + size_t(a.stages) * split_stage_bytes(p.bn) + 256;
+  cudaError_t e = cudaFuncSetAttribute(k_mx4_split, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  launch_cfg(cfg, attr, static_cast<unsigned>(p.n_tiles * p.splits), static_cast<unsigned>(p.t_tiles), kSplitThreads, smem,
+             p.splits, st);
+  return cudaLaunchKernelEx(&cfg, k_mx4_split, tm_w, tm_x, a);
 }
 
 }  // namespace qe

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
   __shared__ double sum_s[32];
   __shared__ uint32_t top_s[32];
   __shared__ float rstd_s;
+  grid_dep_launch();  // the projection's product may set itself up meanwhile
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   const int KT = (a.d + kMxTileCols - 1) / kMxTileCols;
   Raw8<BF16> x[VPT], q[VPT];

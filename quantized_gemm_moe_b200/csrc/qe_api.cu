@@ -380,9 +380,9 @@ qe_status check_mx4_product(int32_t T, int32_t d_in, int32_t d_out, qe_dtype yd)
   return QE_OK;
 }
 
-// Both operands quantized; T > 0 and everything checked.
+// Both operands quantized; T > 0 and everything checked. w_early: see launch_mx4_pair.
 qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
-                           int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype yd, cudaStream_t st) {
+                           int32_t T, int32_t d_in, int32_t d_out, void* Y, qe_dtype yd, bool w_early, cudaStream_t st) {
   const Mx4Plan p = plan_mx4(T, d_out, d_in);
   CUtensorMap tm_w, tm_x;
   qe_status s;
@@ -404,14 +404,15 @@ qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void
                               bf ? 2 : 4, d_out, T, 32, 32, bf ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) !=
                    QE_OK)
       return s;
-    QE_CUDA(launch_mx4_pair(tm_w, tm_x, tm_ws, tm_xs, tma ? &tm_y : nullptr, p, T, d_out, d_in, Y, yd == QE_BF16, device_error_ptr(), st),
+    QE_CUDA(launch_mx4_pair(tm_w, tm_x, tm_ws, tm_xs, tma ? &tm_y : nullptr, p, T, d_out, d_in, Y, bf, w_early,
+                            device_error_ptr(), st),
             "mx4_pair");
     return QE_OK;
   }
   if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128, p.bn)) != QE_OK) return s;
-  QE_CUDA(launch_mx4_product(tm_w, tm_x, p, static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(x_scales),
-                             T, d_out, d_in, Y, yd == QE_BF16, device_error_ptr(), st),
-          "mx4_product");
+  QE_CUDA(launch_mx4_split(tm_w, tm_x, p, static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(x_scales), T,
+                           d_out, d_in, Y, yd == QE_BF16, w_early, device_error_ptr(), st),
+          "mx4_split");
   return QE_OK;
 }
 
@@ -769,7 +770,7 @@ qe_status qe_mx4_product(const void* x_codes, const void* x_scales, const void* 
   if (!x_codes || !x_scales || !Y) return QE_ERR_INVALID_ARG;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
     return QE_ERR_ALIGNMENT;
-  return mx4_product_impl(x_codes, x_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype,
+  return mx4_product_impl(x_codes, x_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype, false,
                           static_cast<cudaStream_t>(stream));
 }
 
@@ -794,7 +795,8 @@ qe_status qe_mx4_linear_forward(const void* w_codes, const void* w_scales, const
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   QE_CUDA(launch_mx4_quantize(X, x_dtype == QE_BF16, s_inv, T, d_in, codes, codes + w.off_scales, cs), "mx4_quantize");
-  return mx4_product_impl(codes, codes + w.off_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype, cs);
+  // the quantization begins after all earlier work on the stream, so the weights are there when it has begun
+  return mx4_product_impl(codes, codes + w.off_scales, w_codes, w_scales, T, d_in, d_out, Y, y_dtype, true, cs);
 }
 
 qe_status qe_split_channels(const int32_t* hist, int32_t d_in, int32_t k, int32_t C, int32_t* channel_pos,

@@ -245,8 +245,9 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 
 // How the MXFP4 product runs. pair: persistent pairs of CTAs over tiles of 256 tokens x 256 output channels; all
 // boxes are 128 rows of codes, tm_ws 2 and tm_xs 1 rows of scale tiles, tm_y 32 x 32 elements (null where Y's rows are
-// no multiple of 16 bytes). Otherwise tiles of 128 output
-// channels x bn tokens, K split over clusters of `splits` CTAs; tm_w boxes are 128 rows, tm_x boxes bn.
+// no multiple of 16 bytes). Otherwise tiles of 128 output channels x bn tokens, K split over clusters of `splits`
+// CTAs; tm_w boxes are 128 rows, tm_x boxes bn. w_early: the weights may be read before the previous kernel on the
+// stream has ended.
 struct Mx4Plan {
   bool pair;
   int bn, n_tiles, t_tiles, splits, ctas;
@@ -254,10 +255,10 @@ struct Mx4Plan {
 Mx4Plan plan_mx4(int T, int N, int K);
 cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const CUtensorMap& tm_ws,
                             const CUtensorMap& tm_xs, const CUtensorMap* tm_y, const Mx4Plan& p, int T, int N, int K,
-                            void* Y, bool y_bf16, int* err, cudaStream_t st);
-cudaError_t launch_mx4_product(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
-                               const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, int* err,
-                               cudaStream_t st);
+                            void* Y, bool y_bf16, bool w_early, int* err, cudaStream_t st);
+cudaError_t launch_mx4_split(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
+                             const uint8_t* x_scales, int T, int N, int K, void* Y, bool y_bf16, bool w_early, int* err,
+                             cudaStream_t st);
 
 // Top-k importance. bf16 rows with 7680 <= K <= 30720 take the streaming kernel (one CTA per
 // SM, rows staged by bulk copies); others, and rows it leaves unresolved, the radix-select kernel.
