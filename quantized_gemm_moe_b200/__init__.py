@@ -361,6 +361,24 @@ def _scratch(shape, dtype, like):
     return torch.empty(shape, dtype=dtype or torch.uint8, device=like.device)
 
 
+def _raise(status: int, what: str, detail: str):
+    raise QEError(status, what, detail)
+
+
+@functools.cache
+def _native():
+    """The extension module of the operators below (csrc/qe_torch.cpp): it checks types, shapes, layout and
+    devices and makes the library's call on the tensors' device, with its current stream unless one is given."""
+    load()
+    import torch  # noqa: F401  (the module's symbols)
+    try:
+        from . import _qe_torch
+    except ImportError as e:
+        raise QEError(-1, "load", f"{e}; build it with `python -m quantized_gemm_moe_b200.build`") from e
+    _qe_torch.set_raise(_raise)
+    return _qe_torch
+
+
 def add_rmsnorm_quant(X, gamma, eps, a_bits, codes=None, scales=None, residual=None, residual_out=None, Y=None,
                       s_inv=None, stream=None):
     """RMS norm of X + residual, with the normed row in Y and quantized into codes and scales.
@@ -368,32 +386,13 @@ def add_rmsnorm_quant(X, gamma, eps, a_bits, codes=None, scales=None, residual=N
     a_bits 8/6: codes int8 [T, d], scales fp32 [T]; 4: MXFP4 codes uint8 [T, d/2] and mx4_scale_bytes(T, d)
     scale bytes; 16: neither.
     """
-    import torch
-    T, d = _rows(X, "X")
-    _expect(gamma, gamma.dtype, (d,), "gamma")
-    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (Y, "Y")):
-        if t is not None:
-            _expect(t, X.dtype, (T, d), name)
-    if s_inv is not None:
-        _expect(s_inv, torch.float32, (d,), "s_inv")
-    if a_bits == 4 and codes is not None and scales is not None:
-        _expect(codes, torch.uint8, (T, d // 2), "codes")
-        _expect(scales, torch.uint8, mx4_scale_bytes(T, d), "scales")
-    elif a_bits in (6, 8) and codes is not None and scales is not None:
-        _expect(codes, torch.int8, (T, d), "codes")
-        _expect(scales, torch.float32, (T,), "scales")
-    _launch("qe_add_rmsnorm_quant", stream, X, _dtype(X), residual, gamma, _dtype(gamma), float(eps), T, d, s_inv,
-            a_bits, residual_out, Y, codes, scales)
+    _native().add_rmsnorm_quant(X, gamma, eps, a_bits, codes, scales, residual, residual_out, Y, s_inv,
+                                None if stream is None else _stream(stream))
 
 
 def act_dequant(codes, sa, out, stream=None):
     """out = codes * sa per token (fp32 or bf16)."""
-    import torch
-    T, d = _rows(codes, "codes")
-    _expect(codes, torch.int8, (T, d), "codes")
-    _expect(sa, torch.float32, (T,), "sa")
-    _expect(out, out.dtype, (T, d), "out")
-    _launch("qe_act_dequant", stream, codes, sa, T, d, out, _dtype(out))
+    _native().act_dequant(codes, sa, out, None if stream is None else _stream(stream))
 
 
 def mx4_code_bytes(rows: int, cols: int) -> int:
@@ -408,35 +407,17 @@ def mx4_scale_bytes(rows: int, cols: int) -> int:
 def mx4_quantize(X, codes, scales, s=None, s_inv=None, stream=None):
     """MXFP4 of fl32(X * s): codes uint8 [rows, cols/2], scales uint8 [mx4_scale_bytes(rows, cols)].
     s_inv (fp32 [cols], with s) receives fl32(1/s)."""
-    import torch
-    rows, cols = _rows(X, "X")
-    _expect(codes, torch.uint8, (rows, cols // 2), "codes")
-    _expect(scales, torch.uint8, mx4_scale_bytes(rows, cols), "scales")
-    for t, name in ((s, "s"), (s_inv, "s_inv")):
-        if t is not None:
-            _expect(t, torch.float32, (cols,), name)
-    _launch("qe_mx4_quantize", stream, X, _dtype(X), s, rows, cols, codes, scales, s_inv)
+    _native().mx4_quantize(X, codes, scales, s, s_inv, None if stream is None else _stream(stream))
 
 
 def mx4_dequantize(codes, scales, out, stream=None):
     """The values of MXFP4 codes, in out's type (fp32 or bf16)."""
-    import torch
-    rows, cols = _rows(out, "out")
-    _expect(codes, torch.uint8, (rows, cols // 2), "codes")
-    _expect(scales, torch.uint8, mx4_scale_bytes(rows, cols), "scales")
-    _launch("qe_mx4_dequantize", stream, codes, scales, rows, cols, out, _dtype(out))
+    _native().mx4_dequantize(codes, scales, out, None if stream is None else _stream(stream))
 
 
 def mx4_product(x_codes, x_scales, w_codes, w_scales, Y, stream=None):
     """Y [T, d_out] = X . W^T of two MXFP4 matrices."""
-    import torch
-    T, N = _rows(Y, "Y")
-    K = 2 * _rows(w_codes, "w_codes")[1]
-    _expect(x_codes, torch.uint8, (T, K // 2), "x_codes")
-    _expect(w_codes, torch.uint8, (N, K // 2), "w_codes")
-    _expect(x_scales, torch.uint8, mx4_scale_bytes(T, K), "x_scales")
-    _expect(w_scales, torch.uint8, mx4_scale_bytes(N, K), "w_scales")
-    _launch("qe_mx4_product", stream, x_codes, x_scales, w_codes, w_scales, T, K, N, Y, _dtype(Y))
+    _native().mx4_product(x_codes, x_scales, w_codes, w_scales, Y, None if stream is None else _stream(stream))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -446,16 +427,7 @@ def mx4_linear_workspace_bytes(T: int, d_in: int) -> int:
 
 def mx4_linear_forward(w_codes, w_scales, X, Y, workspace, s_inv=None, stream=None):
     """Y = MXFP4(X * s_inv) . W^T for an MXFP4 W."""
-    import torch
-    T, K = _rows(X, "X")
-    N = _rows(Y, "Y")[1]
-    _expect(Y, Y.dtype, (T, N), "Y")
-    _expect(w_codes, torch.uint8, (N, K // 2), "w_codes")
-    _expect(w_scales, torch.uint8, mx4_scale_bytes(N, K), "w_scales")
-    if s_inv is not None:
-        _expect(s_inv, torch.float32, (K,), "s_inv")
-    _launch("qe_mx4_linear_forward", stream, w_codes, w_scales, s_inv, X, _dtype(X), T, K, N, Y, _dtype(Y), workspace,
-            workspace.numel() * workspace.element_size())
+    _native().mx4_linear_forward(w_codes, w_scales, X, Y, workspace, s_inv, None if stream is None else _stream(stream))
 
 
 def device_error(clear: bool = True, stream=None) -> int:

@@ -4,6 +4,8 @@
 
 Every .cu under csrc/ is compiled with nvcc for sm_100a and linked into one
 shared library next to this file. The C ABI is declared in include/qe.h.
+csrc/qe_torch.cpp, the binding of the norm and MXFP4 operators for torch
+tensors, becomes the extension module _qe_torch.so beside it.
 """
 from __future__ import annotations
 
@@ -17,6 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqe.so")
+BINDING_SRC = os.path.join(CSRC, "qe_torch.cpp")
+BINDING = os.path.join(HERE, "_qe_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -36,15 +40,40 @@ def _inputs() -> list[str]:
         [os.path.join(ROOT, "include", "qe.h")]
 
 
+def _newer(out: str, inputs: list[str]) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in inputs)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def build_binding(force: bool = False) -> str:
+    """g++ against torch's headers; libqe.so is found next to the module."""
+    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "qe.h")]):
+        return BINDING
+    import sysconfig
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", BINDING_SRC, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(t, "include"), "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+           "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L" + HERE, "-l:libqe.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        sys.stdout.write(r.stdout.decode(errors="replace"))
+        raise RuntimeError("g++ failed for " + BINDING_SRC)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and up_to_date():
+        build_binding()
         return LIB
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -72,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-ldl", "-lrt", "-lpthread"],
                    check=True)
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
