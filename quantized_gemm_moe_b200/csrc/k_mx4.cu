@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "qe_internal.h"
+#include "qe_launch.cuh"
 #include "qe_ptx.cuh"
 #include "qe_quant.cuh"
 
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const void* __re
                                                                 int rows, int cols, int spans, size_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
+  grid_dep_wait();
   grid_dep_launch();  // a product may set itself up, and load its weights, meanwhile
   const int lane = threadIdx.x & 31;
   const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
@@ -126,6 +128,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t*
                                                                   const uint8_t* __restrict__ scales, int cols,
                                                                   int spans, size_t units, void* __restrict__ out,
                                                                   int out_bf16) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
@@ -178,8 +182,7 @@ cudaError_t launch_mx4_quantize(const void* X, bool x_bf16, const float* s, int 
   const unsigned grid = static_cast<unsigned>(ceil_div(units, kQuantThreads / 32));
   auto k = x_bf16 ? (s ? k_mx4_quantize<true, true> : k_mx4_quantize<true, false>)
                   : (s ? k_mx4_quantize<false, true> : k_mx4_quantize<false, false>);
-  k<<<grid, kQuantThreads, 0, st>>>(X, s, rows, cols, spans, units, codes, scales);
-  return cudaGetLastError();
+  return launch_dependent(k, dim3(grid), kQuantThreads, 0, 1, st, X, s, rows, cols, spans, units, codes, scales);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
@@ -187,9 +190,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
   if (rows == 0) return cudaSuccess;
   const int spans = static_cast<int>(ceil_div(cols, kDequantSpan));
   const size_t units = static_cast<size_t>(rows) * spans;
-  k_mx4_dequantize<<<static_cast<unsigned>(ceil_div(units, kQuantThreads / 32)), kQuantThreads, 0, st>>>(
-      codes, scales, cols, spans, units, out, out_bf16);
-  return cudaGetLastError();
+  return launch_dependent(k_mx4_dequantize, dim3(static_cast<unsigned>(ceil_div(units, kQuantThreads / 32))), kQuantThreads, 0,
+                          1, st, codes, scales, cols, spans, units, out, static_cast<int>(out_bf16));
 }
 
 }  // namespace qe

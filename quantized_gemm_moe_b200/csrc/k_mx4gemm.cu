@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "qe_internal.h"
+#include "qe_launch.cuh"
 #include "qe_ptx.cuh"
 #include "qe_quant.cuh"
 
@@ -482,23 +483,6 @@ __global__ void __launch_bounds__(kPairThreads)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-cudaError_t launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned gx, unsigned gy, int threads,
-                       size_t smem, int cluster, cudaStream_t st) {
-  cfg.gridDim = dim3(gx, gy);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaSuccess;
-}
-
 }  // namespace
 
 Mx4Plan plan_mx4(int T, int N, int K) {
@@ -546,10 +530,8 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
   a.tma = tm_y != nullptr;
   a.w_early = w_early;
   a.err = err;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  launch_cfg(cfg, attr, p.ctas, 1, kPairThreads, C::kSmem, 2, st);
-  return cudaLaunchKernelEx(&cfg, k_mx4_pair, tm_x, tm_w, tm_xs, tm_ws, tm_y ? *tm_y : tm_x, a);
+  return launch_dependent(k_mx4_pair, dim3(static_cast<unsigned>(p.ctas)), kPairThreads, C::kSmem, 2, st, tm_x, tm_w, tm_xs,
+                          tm_ws, tm_y ? *tm_y : tm_x, a);
 }
 
 cudaError_t launch_mx4_split(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const Mx4Plan& p, const uint8_t* w_scales,
@@ -575,11 +557,8 @@ cudaError_t launch_mx4_split(const CUtensorMap& tm_w, const CUtensorMap& tm_x, c
   const size_t smem = 1024 + size_t(a.stages) * split_stage_bytes(p.bn) + 256;
   cudaError_t e = cudaFuncSetAttribute(k_mx4_split, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  launch_cfg(cfg, attr, static_cast<unsigned>(p.n_tiles * p.splits), static_cast<unsigned>(p.t_tiles), kSplitThreads, smem,
-             p.splits, st);
-  return cudaLaunchKernelEx(&cfg, k_mx4_split, tm_w, tm_x, a);
+  return launch_dependent(k_mx4_split, dim3(static_cast<unsigned>(p.n_tiles * p.splits), static_cast<unsigned>(p.t_tiles)),
+                          kSplitThreads, smem, p.splits, st, tm_w, tm_x, a);
 }
 
 }  // namespace qe

@@ -1,6 +1,7 @@
 // The residual's addition and the root-mean-square norm in front of a quantized projection, with the
 // normed row quantized in the same pass, and the dequantization of per-token int8 codes.
 #include "qe_internal.h"
+#include "qe_launch.cuh"
 #include "qe_ptx.cuh"
 #include "qe_quant.cuh"
 
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
   __shared__ double sum_s[32];
   __shared__ uint32_t top_s[32];
   __shared__ float rstd_s;
-  grid_dep_launch();  // the projection's product may set itself up meanwhile
+  grid_dep_wait();
+  grid_dep_launch();  // the projection may set itself up meanwhile
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   const int KT = (a.d + kMxTileCols - 1) / kMxTileCols;
   Raw8<BF16> x[VPT], q[VPT];
@@ -236,6 +238,8 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
 constexpr int kDequantSteps = 4;
 __global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ codes, const float* __restrict__ sa,
                                                      uint32_t d8, uint32_t n8, void* __restrict__ out, int out_bf16) {
+  grid_dep_wait();
+  grid_dep_launch();
   const uint32_t i0 = blockIdx.x * (256u * kDequantSteps) + threadIdx.x;
   uint2 w[kDequantSteps];
   float s[kDequantSteps];
@@ -267,8 +271,7 @@ cudaError_t launch_norm_t(const NormArgs& a, int out, cudaStream_t st) {
   auto k = out == kOutInt8 ? k_add_rmsnorm<BF16, VPT, kOutInt8>
            : out == kOutMx4 ? k_add_rmsnorm<BF16, VPT, kOutMx4>
                             : k_add_rmsnorm<BF16, VPT, kOutNone>;
-  k<<<a.T, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(k, dim3(static_cast<unsigned>(a.T)), threads, 0, 1, st, a);
 }
 
 // Vectors per thread. With at most two rows per SM latency counts, and a row takes as many threads as it has
@@ -314,9 +317,8 @@ cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int 
   const size_t n8 = static_cast<size_t>(T) * (d / 8);
   if (n8 == 0) return cudaSuccess;
   if (n8 > 0xFFFF0000u) return cudaErrorInvalidValue;  // 32 G elements
-  k_act_dequant<<<static_cast<unsigned>(ceil_div(n8, 256 * kDequantSteps)), 256, 0, st>>>(
-      codes, sa, static_cast<uint32_t>(d / 8), static_cast<uint32_t>(n8), out, out_bf16);
-  return cudaGetLastError();
+  return launch_dependent(k_act_dequant, dim3(static_cast<unsigned>(ceil_div(n8, 256 * kDequantSteps))), 256, 0, 1, st, codes, sa,
+                          static_cast<uint32_t>(d / 8), static_cast<uint32_t>(n8), out, static_cast<int>(out_bf16));
 }
 
 }  // namespace qe
