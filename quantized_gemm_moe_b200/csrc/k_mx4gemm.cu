@@ -1,5 +1,6 @@
 // Product of MXFP4 activations and MXFP4 weights on the block-scaled 4-bit tensor cores.
 #include <algorithm>
+#include <atomic>
 
 #include "qe_internal.h"
 #include "qe_launch.cuh"
@@ -10,12 +11,32 @@ namespace qe {
 namespace {
 
 constexpr int kMxStageK = 256;  // channels per pipeline stage: 128 bytes of codes, one swizzle row
+// Y[t][n .. n+4) = v, as far as the row of N channels reaches.
+__device__ __forceinline__ void store4(void* Y, int y_bf16, int N, int t, int n, const float4& v) {
+  const size_t y = static_cast<size_t>(t) * N + n;
+  if ((N & 3) == 0) {
+    if (n < N) {
+      if (y_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + y) = make_uint2(bf16x2_word(v.x, v.y), bf16x2_word(v.z, v.w));
+      else *reinterpret_cast<float4*>(static_cast<float*>(Y) + y) = v;
+    }
+  } else {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j < N) {
+        if (y_bf16) static_cast<uint16_t*>(Y)[y + j] = f32_to_bf16_bits(f[j]);
+        else static_cast<float*>(Y)[y + j] = f[j];
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ few tokens
 struct SplitArgs {
   const uint8_t* w_scales;
   const uint8_t* x_scales;
   int T, N, K, KT;      // KT = ceil(K / 128) scale tiles along K
-  int bn, nb, splits;   // tokens per tile (a multiple of 16), scale tiles across them, CTAs along K
+  int bn, splits;       // MMA columns: T rounded up to 16, at most 128; CTAs along K
   int stages, tmem_cols;
   int w_early;          // the weights were written before the previous kernel began
   void* Y;
@@ -25,54 +46,59 @@ struct SplitArgs {
 constexpr int kSplitThreads = 192;
 constexpr int kSplitA = 16384, kSplitSA = 1024;
 
-__host__ __device__ constexpr int split_stage_bytes(int bn) { return kSplitA + bn * 128 + kSplitSA + 1024 * ((bn + 127) / 128); }
-__host__ __device__ constexpr int split_sf_cols(int nb) { return 8 + 8 * nb; }  // tensor memory columns of a stage's scales
-// Room for two CTAs on an SM up to 128 tokens, and for one above.
-constexpr int split_stages(int bn) { return (bn <= 128 ? 114176 : 230912) / split_stage_bytes(bn); }
+constexpr int kSplitSfCols = 16;  // tensor memory columns of a stage's scales
+__host__ __device__ constexpr int split_stage_bytes(int bn) { return kSplitA + bn * 128 + 2 * kSplitSA; }
+// Two CTAs share an SM's 228 KB.
+constexpr int split_stages(int bn) { return 114176 / split_stage_bytes(bn); }
 
-// Adds the cluster's partial tiles in rank order, four channels of a token at a time, and writes this CTA's
-// share of them.
-template <int S>
-__device__ __forceinline__ void split_reduce(const SplitArgs& a, uint32_t part, int rank, int n0, int t0, int ncols) {
-  uint32_t from[S];
+// v = the sum in rank order of four floats at `at` in each of S CTAs' partial tiles, for U addresses at once (eight
+// 16-byte loads of distributed shared memory in flight: one at a time, their latency was half of a short call).
+template <int S, int U>
+__device__ __forceinline__ void sum_parts(const uint32_t (&from)[S], const uint32_t (&at)[U], float4 (&v)[U]) {
+  float4 p[U][S];
 #pragma unroll
-  for (int r = 0; r < S; ++r) from[r] = S > 1 ? mapa(part, r) : part;
-  const int total = ncols * 32;
-  const int i1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / S);
-  for (int i = static_cast<int>(static_cast<int64_t>(total) * rank / S) + threadIdx.x; i < i1; i += kSplitThreads) {
-    float4 p[S];
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int r = 0; r < S; ++r) p[r] = ld_cluster_f32x4(from[r] + i * 16);
-    float4 v = p[0];
+    for (int r = 0; r < S; ++r) p[u][r] = ld_cluster_f32x4(from[r] + at[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    v[u] = p[u][0];
 #pragma unroll
     for (int r = 1; r < S; ++r) {
-      v.x += p[r].x;
-      v.y += p[r].y;
-      v.z += p[r].z;
-      v.w += p[r].w;
-    }
-    const int n = n0 + (i & 31) * 4;
-    const size_t y = static_cast<size_t>(t0 + (i >> 5)) * a.N + n;
-    if ((a.N & 3) == 0) {
-      if (n < a.N) {
-        if (a.y_bf16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.Y) + y) = make_uint2(bf16x2_word(v.x, v.y), bf16x2_word(v.z, v.w));
-        else *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + y) = v;
-      }
-    } else {
-      const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (n + j < a.N) {
-          if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y + j] = f32_to_bf16_bits(f[j]);
-          else static_cast<float*>(a.Y)[y + j] = f[j];
-        }
-      }
+      v[u].x += p[u][r].x;
+      v[u].y += p[u][r].y;
+      v[u].z += p[u][r].z;
+      v[u].w += p[u][r].w;
     }
   }
 }
 
-// Y tile of 128 output channels (MMA rows) x bn tokens (MMA columns), the K range split over the cluster's
-// CTAs, whose fp32 partial tiles are then added in rank order through distributed shared memory.
+// Adds the cluster's partial tiles, four channels of a token at a time, and writes this CTA's share of them.
+template <int S>
+__device__ __forceinline__ void split_reduce(const SplitArgs& a, uint32_t part, int rank, int n0) {
+  constexpr int U = 8 / S;
+  uint32_t from[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) from[r] = S > 1 ? mapa(part, r) : part;
+  const int total = a.T * 32;
+  const int i0 = static_cast<int>(static_cast<int64_t>(total) * rank / S), i1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / S);
+  for (int i = i0 + threadIdx.x; i < i1; i += kSplitThreads * U) {
+    uint32_t at[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) at[u] = 16 * min(i + u * kSplitThreads, i1 - 1);
+    sum_parts<S, U>(from, at, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = i + u * kSplitThreads;
+      if (j < i1) store4(a.Y, a.y_bf16, a.N, j >> 5, n0 + (j & 31) * 4, v[u]);
+    }
+  }
+}
+
+// At most 128 tokens. Y tile of 128 output channels (MMA rows) x all tokens (MMA columns), the K range split over
+// the cluster's CTAs, whose fp32 partial tiles are then added in rank order through distributed shared memory.
 // Weights stream once through each CTA's ring of TMA stages, so few tokens are bound by HBM; clusters make
 // enough CTAs to keep all SMs streaming when there are few tiles.
 __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_constant__ CUtensorMap tm_w,
@@ -80,18 +106,17 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
                                                              const SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int NS = a.stages, kB = a.bn * 128, stage = split_stage_bytes(a.bn), sf_cols = split_sf_cols(a.nb);
+  const int NS = a.stages, kB = a.bn * 128, stage = split_stage_bytes(a.bn);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * stage);
   uint64_t* empty = full + NS;
   uint64_t* accf = empty + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int n_tile = blockIdx.x / a.splits, n0 = n_tile * 128, t0 = blockIdx.y * a.bn;
+  const int n_tile = blockIdx.x / a.splits, n0 = n_tile * 128;
   const int KS = (a.K + kMxStageK - 1) / kMxStageK;
   const int s0 = static_cast<int>(static_cast<int64_t>(KS) * rank / a.splits);
   const int nk = static_cast<int>(static_cast<int64_t>(KS) * (rank + 1) / a.splits) - s0;
-  const int ncols = min(a.bn, a.T - t0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -114,14 +139,11 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
 
   if (warp == 0) {
     if (lane == 0) {
-      // scale tiles of the token tile: the first may start inside a 128-row tile only when it is the only one
-      const size_t rb = t0 / 128;
-      const int nb = min(a.nb, static_cast<int>((a.T + 127) / 128 - rb));
       auto load_w = [&](int it) {
         const int s = it % NS, ks = s0 + it;
         uint8_t* st = smem + s * stage;
         const uint32_t sf = kMxTileBytes * min(2, a.KT - 2 * ks);
-        mbar_arrive_expect_tx(&full[s], kSplitA + kB + sf * (1 + nb));
+        mbar_arrive_expect_tx(&full[s], kSplitA + kB + 2 * sf);
         tma_load_2d(st, &tm_w, ks * 128, n0, &full[s]);
         bulk_load(st + kSplitA + kB, a.w_scales + (static_cast<size_t>(n_tile) * a.KT + 2 * ks) * kMxTileBytes, sf, &full[s]);
       };
@@ -129,9 +151,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
         const int s = it % NS, ks = s0 + it;
         uint8_t* st = smem + s * stage;
         const uint32_t sf = kMxTileBytes * min(2, a.KT - 2 * ks);
-        tma_load_2d(st + kSplitA, &tm_x, ks * 128, t0, &full[s]);
-        for (int b = 0; b < nb; ++b)
-          bulk_load(st + kSplitA + kB + kSplitSA + 1024 * b, a.x_scales + ((rb + b) * a.KT + 2 * ks) * kMxTileBytes, sf, &full[s]);
+        tma_load_2d(st + kSplitA, &tm_x, ks * 128, 0, &full[s]);
+        bulk_load(st + kSplitA + kB + kSplitSA, a.x_scales + static_cast<size_t>(2 * ks) * kMxTileBytes, sf, &full[s]);
       };
       const int ahead = min(nk, NS);
       if (!a.w_early) grid_dep_wait();
@@ -156,13 +177,12 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
       tc_fence_after();
       if (leader) {
         const uint32_t at = smem_u32(smem + s * stage);
-        const uint32_t sfa = tmem + a.bn + (it & 1) * sf_cols, sfb = sfa + 8;
+        const uint32_t sfa = tmem + a.bn + (it & 1) * kSplitSfCols, sfb = sfa + 8;
         const int tiles = min(2, a.KT - 2 * ks);
         const uint32_t sa = at + kSplitA + kB, sb = sa + kSplitSA;
         for (int k = 0; k < tiles; ++k) {
           tmem_cp_32x128b(sfa + 4 * k, smem_desc_rows16(sa + k * kMxTileBytes));
-          for (int b = 0; b < a.nb; ++b)
-            tmem_cp_32x128b(sfb + (k * a.nb + b) * 4, smem_desc_rows16(sb + b * 1024 + k * kMxTileBytes));
+          tmem_cp_32x128b(sfb + 4 * k, smem_desc_rows16(sb + k * kMxTileBytes));
         }
         const uint64_t da = smem_desc_sw128(at), db = smem_desc_sw128(at + kSplitA);
         const int mmas = min(4, (a.K - ks * kMxStageK + 63) / 64);
@@ -171,7 +191,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
           const uint32_t sel = static_cast<uint32_t>(m & 1) * 2;
           if (m < mmas)
             mma_mxf4(tmem, da + 2 * m, db + 2 * m, id | (sel << 29) | (sel << 4), sfa + 4 * (m >> 1),
-                     sfb + 4 * a.nb * (m >> 1), (it | m) != 0);
+                     sfb + 4 * (m >> 1), (it | m) != 0);
         }
         tc_commit(&empty[s]);
         if (it == nk - 1) tc_commit(accf);
@@ -184,7 +204,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
     float* part = reinterpret_cast<float*>(smem);
     if (__all_sync(0xffffffffu, mbar_wait(accf, 0, a.err, DEVERR_WAIT_EPILOGUE))) {
       tc_fence_after();
-      for (int c0 = 0; c0 < ncols; c0 += 16) {
+      for (int c0 = 0; c0 < a.T; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c0, v);
         tmem_wait_ld();
@@ -199,10 +219,10 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
   else __syncthreads();
   const uint32_t part = smem_u32(smem);
   switch (a.splits) {
-    case 1: split_reduce<1>(a, part, rank, n0, t0, ncols); break;
-    case 2: split_reduce<2>(a, part, rank, n0, t0, ncols); break;
-    case 4: split_reduce<4>(a, part, rank, n0, t0, ncols); break;
-    default: split_reduce<8>(a, part, rank, n0, t0, ncols); break;
+    case 1: split_reduce<1>(a, part, rank, n0); break;
+    case 2: split_reduce<2>(a, part, rank, n0); break;
+    case 4: split_reduce<4>(a, part, rank, n0); break;
+    default: split_reduce<8>(a, part, rank, n0); break;
   }
   if (a.splits > 1) cluster_sync_all();  // no CTA leaves while another may still read its partial tile
   else __syncthreads();
@@ -313,6 +333,34 @@ __device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap*
   }
 }
 
+// Adds the K slices' partial tiles (fp32 rows of 256 columns, 16-byte pieces permuted by the row) and stores this
+// slice's share of the CTA's 128 rows.
+template <int S>
+__device__ __forceinline__ void pair_reduce(const PairArgs& a, uint32_t part, int cta, int slice, int m0, int n0) {
+  constexpr int U = 8 / S, total = 128 / S * 64;
+  uint32_t from[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) from[r] = mapa(part, cta + 2 * r);
+  for (int i = threadIdx.x; i < total; i += kPairThreads * U) {
+    uint32_t at[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(i + u * kPairThreads, total - 1), row = 128 / S * slice + (j >> 6);
+      at[u] = static_cast<uint32_t>(row * 1024 + (((j & 63) ^ (row & 7)) * 16));
+    }
+    sum_parts<S, U>(from, at, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = i + u * kPairThreads, row = m0 + 128 / S * slice + (j >> 6);
+      if (j < total && row < a.T) store4(a.Y, a.y_bf16, a.N, row, n0 + 4 * (j & 63), v[u]);
+    }
+  }
+}
+
+// S > 1: a cluster of S pairs takes one tile, a slice of K each, and adds the slices' partial tiles through
+// distributed shared memory: few tiles with a long K then use more SMs.
+template <int S>
 __global__ void __launch_bounds__(kPairThreads)
     k_mx4_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
@@ -328,9 +376,12 @@ __global__ void __launch_bounds__(kPairThreads)
   uint64_t* freed = accf + 2;    // the shared columns of a tile are drained (even CTA's, from both CTAs)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(freed + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = static_cast<int>(cluster_ctarank());
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int KS = (a.K + kMxStageK - 1) / kMxStageK;
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int cta = crank & 1, lead = crank & ~1, slice = crank >> 1;
+  const int pair = blockIdx.x / (2 * S), pairs = gridDim.x / (2 * S);
+  const int KS_all = (a.K + kMxStageK - 1) / kMxStageK;
+  const int ks0 = static_cast<int>(static_cast<int64_t>(KS_all) * slice / S);
+  const int KS = static_cast<int>(static_cast<int64_t>(KS_all) * (slice + 1) / S) - ks0;
   const int tiles = a.m_tiles * a.n_tiles;
 
   if (threadIdx.x == 0) {
@@ -365,14 +416,16 @@ __global__ void __launch_bounds__(kPairThreads)
         const int s = it % NS;
         uint8_t* st = smem + s * C::kStage;
         if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
-        const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+        const uint32_t bar = mapa(smem_u32(&full[s]), lead);
+        ks += ks0;
         tma_load_2d_pair(st + C::kA, &tm_w, ks * 128, nt * 256 + cta * 128, bar);
         tma_load_2d_pair(st + C::kA + C::kB + C::kSA, &tm_ws, ks * 256, nt * 2, bar);
       };
       auto load_x = [&](int it, int ks, int mt) {
         const int s = it % NS;
         uint8_t* st = smem + s * C::kStage;
-        const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+        const uint32_t bar = mapa(smem_u32(&full[s]), lead);
+        ks += ks0;
         tma_load_2d_pair(st, &tm_x, ks * 128, mt * 256 + cta * 128, bar);
         tma_load_2d_pair(st + C::kA + C::kB, &tm_xs, ks * 256, mt * 2 + cta, bar);
       };
@@ -430,7 +483,7 @@ __global__ void __launch_bounds__(kPairThreads)
                 tmem_cp_32x128b_pair(sfb + (2 * k + b) * 4, smem_desc_rows16(sb + b * 1024 + k * kMxTileBytes));
             }
             const uint64_t da = smem_desc_sw128(at), db = smem_desc_sw128(at + C::kA);
-            const int mmas = min(4, (a.K - ks * kMxStageK + 63) / 64);
+            const int mmas = min(4, (a.K - (ks0 + ks) * kMxStageK + 63) / 64);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const uint32_t sel = static_cast<uint32_t>(m & 1) * 2;
@@ -438,8 +491,8 @@ __global__ void __launch_bounds__(kPairThreads)
                 mma_mxf4_pair(acc, da + 2 * m, db + 2 * m, id | (sel << 29) | (sel << 4), sfa + 4 * (m >> 1),
                               sfb + 8 * (m >> 1), (ks | m) != 0);
             }
-            tc_commit_pair(&empty[s]);
-            if (ks == KS - 1) tc_commit_pair(&accf[n & 1]);
+            tc_commit_pair(&empty[s], lead);
+            if (ks == KS - 1) tc_commit_pair(&accf[n & 1], lead);
           }
           __syncwarp();
         }
@@ -447,11 +500,29 @@ __global__ void __launch_bounds__(kPairThreads)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
+    if constexpr (S > 1) {
+      // this slice's partial tile, over the stages: all of them have been read
+      if (__all_sync(0xffffffffu, mbar_wait(&accf[0], 0, a.err, DEVERR_WAIT_EPILOGUE))) {
+        tc_fence_after();
+        uint8_t* row = smem + (32 * q + lane) * 1024;
+#pragma unroll 1
+        for (int c = half * 128; c < half * 128 + 128; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(row + ((c / 4 + i) ^ (lane & 7)) * 16) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    }
     uint8_t* out = staging + (warp - 2) * C::kOut;
     int turn = 0;
-    const uint32_t freed0 = mapa(smem_u32(freed), 0);
+    const uint32_t freed0 = mapa(smem_u32(freed), lead);
     int n = 0;
-    for (int tile = pair; tile < tiles; tile += pairs, ++n) {
+    for (int tile = pair; S == 1 && tile < tiles; tile += pairs, ++n) {
       int mt, nt;
       pair_tile(a, tile, mt, nt);
       if (!__all_sync(0xffffffffu, mbar_wait(&accf[n & 1], (n >> 1) & 1, a.err, DEVERR_WAIT_EPILOGUE))) break;
@@ -479,36 +550,81 @@ __global__ void __launch_bounds__(kPairThreads)
     tc_fence_before();
   }
   __syncthreads();
-  cluster_sync_all();  // neither CTA frees memory that the other's instructions may still use
+  if constexpr (S > 1) {
+    cluster_sync_all();
+    int mt, nt;
+    pair_tile(a, pair, mt, nt);
+    pair_reduce<S>(a, smem_u32(smem), cta, slice, mt * 256 + cta * 128, nt * 256);
+  }
+  cluster_sync_all();  // no CTA frees memory that the others' instructions may still use
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 }  // namespace
 
+namespace {
+
+// Clusters of 2 * S CTAs of k_mx4_pair<S> that the current device holds at once (looked up once per device).
+template <int S>
+int resident_clusters() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * S);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = PairCfg::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(k_mx4_pair<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PairCfg::kSmem)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_mx4_pair<S>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace
+
+// Up to 128 tokens a tile's MMAs have as many columns as there are tokens, and the split kernel streams weights
+// through all SMs; above, 256 x 256 tiles load less for each product (130 x 4096 -> 6144: 10.7 us, and 11.5 with
+// 144-column tiles; 256 x 8192 -> 8192: 15.6 and 17.8).
 Mx4Plan plan_mx4(int T, int N, int K) {
   Mx4Plan p{};
   int sms = decode_grid_sms();
   if (sms == 0) sms = 148;
-  p.pair = T > 256;
-  if (p.pair) {
-    p.bn = 256;
-    p.n_tiles = static_cast<int>(ceil_div(N, 256));
-    p.t_tiles = static_cast<int>(ceil_div(T, 256));
-    p.splits = 1;
-    p.ctas = static_cast<int>(2 * std::min<int64_t>(sms / 2, static_cast<int64_t>(p.n_tiles) * p.t_tiles));
-    return p;
-  }
-  p.t_tiles = static_cast<int>(ceil_div(T, 256));
-  // several token tiles start on whole scale tiles
-  p.bn = p.t_tiles == 1 ? static_cast<int>(round_up(T, 16)) : 256;
-  p.n_tiles = static_cast<int>(ceil_div(N, 128));
-  // as many CTAs as two per SM (one above 128 tokens) hold, in clusters of at most eight along K
-  const int slots = p.bn > 128 ? sms : 2 * sms;
-  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.t_tiles;
   const int stages = static_cast<int>(ceil_div(K, kMxStageK));
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= slots && p.splits * 2 <= stages) p.splits *= 2;
-  p.ctas = static_cast<int>(tiles * p.splits);
+  p.pair = T > 128;
+  if (p.pair) {
+    p.n_tiles = static_cast<int>(ceil_div(N, 256));
+    p.t_tiles = static_cast<int>(ceil_div(T, 256));
+    const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.t_tiles;
+    // K slices where the tiles leave SMs idle and a slice's saving (0.28 us a stage) exceeds the 2 to 3 us that the
+    // larger cluster and its sum cost: 512 x 8192 -> 1024: 15.0, 12.8 and 11.5 us with 1, 2 and 4 slices;
+    // 512 x 4096 -> 4096: 10.9 and 11.7 with 1 and 2
+    if (stages >= 20) {
+      if (tiles <= resident_clusters<4>()) p.splits = 4;
+      else if (tiles <= resident_clusters<2>()) p.splits = 2;
+    }
+    p.ctas = static_cast<int>(p.splits > 1 ? 2 * p.splits * tiles : 2 * std::min<int64_t>(sms / 2, tiles));
+    return p;
+  }
+  p.n_tiles = static_cast<int>(ceil_div(N, 128));
+  p.t_tiles = 1;
+  // as many CTAs as two per SM hold, in clusters of at most eight along K, with three stages each at least
+  // (128 x 1536 -> 8960: 8.5, 7.9 and 10.5 us with 1, 2 and 4; 1 x 8192 -> 1024: 17.6, 11.1, 7.5 and 5.6 with 1, 2, 4 and 8)
+  while (p.splits < 8 && static_cast<int64_t>(p.n_tiles) * p.splits <= sms && stages >= 6 * p.splits) p.splits *= 2;
+  p.ctas = p.n_tiles * p.splits;
   return p;
 }
 
@@ -516,7 +632,8 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
                             const CUtensorMap& tm_xs, const CUtensorMap* tm_y, const Mx4Plan& p, int T, int N, int K,
                             void* Y, bool y_bf16, bool w_early, int* err, cudaStream_t st) {
   using C = PairCfg;
-  cudaError_t e = cudaFuncSetAttribute(k_mx4_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  auto k = p.splits == 1 ? k_mx4_pair<1> : p.splits == 2 ? k_mx4_pair<2> : k_mx4_pair<4>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
   PairArgs a{};
   a.T = T;
@@ -524,13 +641,17 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
   a.K = K;
   a.m_tiles = p.t_tiles;
   a.n_tiles = p.n_tiles;
-  a.group = std::min(p.t_tiles, 8);
+  // Token tiles walked together while a tile of weights is in use: as many as keep their activations within 36 MB
+  // of L2, in equal groups, so that the weights are read from HBM once for each group (8192 x 8192 -> 29568, sustained:
+  // 776 us in groups of 8, 743 in one of 32; 8192 x 29568 -> 8192: 766 in groups of 8, 825 in one of 32).
+  const int most = static_cast<int>(std::max<int64_t>(1, (int64_t(36) << 20) / (int64_t(256) * K * 17 / 32)));
+  a.group = static_cast<int>(ceil_div(p.t_tiles, ceil_div(p.t_tiles, most)));
   a.Y = Y;
   a.y_bf16 = y_bf16;
   a.tma = tm_y != nullptr;
   a.w_early = w_early;
   a.err = err;
-  return launch_dependent(k_mx4_pair, dim3(static_cast<unsigned>(p.ctas)), kPairThreads, C::kSmem, 2, st, tm_x, tm_w, tm_xs,
+  return launch_dependent(k, dim3(static_cast<unsigned>(p.ctas)), kPairThreads, C::kSmem, 2 * p.splits, st, tm_x, tm_w, tm_xs,
                           tm_ws, tm_y ? *tm_y : tm_x, a);
 }
 
@@ -544,21 +665,19 @@ cudaError_t launch_mx4_split(const CUtensorMap& tm_w, const CUtensorMap& tm_x, c
   a.N = N;
   a.K = K;
   a.KT = static_cast<int>(ceil_div(K, kMxTileCols));
-  a.bn = p.bn;
-  a.nb = static_cast<int>(ceil_div(p.bn, 128));
+  a.bn = static_cast<int>(round_up(T, 16));
   a.splits = p.splits;
-  a.stages = split_stages(p.bn);
-  const int cols = p.bn + 2 * split_sf_cols(a.nb);
-  a.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  a.stages = split_stages(a.bn);
+  const int cols = a.bn + 2 * kSplitSfCols;
+  a.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
   a.w_early = w_early;
   a.Y = Y;
   a.y_bf16 = y_bf16;
   a.err = err;
-  const size_t smem = 1024 + size_t(a.stages) * split_stage_bytes(p.bn) + 256;
-  cudaError_t e = cudaFuncSetAttribute(k_mx4_split, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  const size_t smem = 1024 + size_t(a.stages) * split_stage_bytes(a.bn) + 256;
+  cudaError_t e = cudaFuncSetAttribute(k_mx4_split, cudaFuncAttributeMaxDynamicSharedMemorySize, 114 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_dependent(k_mx4_split, dim3(static_cast<unsigned>(p.n_tiles * p.splits), static_cast<unsigned>(p.t_tiles)),
-                          kSplitThreads, smem, p.splits, st, tm_w, tm_x, a);
+  return launch_dependent(k_mx4_split, dim3(static_cast<unsigned>(p.ctas)), kSplitThreads, smem, p.splits, st, tm_w, tm_x, a);
 }
 
 }  // namespace qe

@@ -409,7 +409,9 @@ qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void
             "mx4_pair");
     return QE_OK;
   }
-  if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128, p.bn)) != QE_OK) return s;
+  if ((s = make_tmap(&tm_x, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d_in / 2, T, 128,
+                     static_cast<uint32_t>(round_up(T, 16)))) != QE_OK)
+    return s;
   QE_CUDA(launch_mx4_split(tm_w, tm_x, p, static_cast<const uint8_t*>(w_scales), static_cast<const uint8_t*>(x_scales), T,
                            d_out, d_in, Y, yd == QE_BF16, w_early, device_error_ptr(), st),
           "mx4_split");

@@ -288,12 +288,13 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
 __device__ __forceinline__ void tmem_cp_32x128b_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs once every tcgen05 op issued so far is done.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+// Arrives on the barrier at this offset in both CTAs of the pair (cluster ranks lead, lead + 1) once every tcgen05 op
+// issued so far is done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, int lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3 << lead))
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
