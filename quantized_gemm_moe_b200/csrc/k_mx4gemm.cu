@@ -269,6 +269,29 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& mt, 
   nt = r / rows;
 }
 
+// Stores a warp's 32 x 32 block of Y from padded rows in shared memory, V elements per lane (N a multiple of V, so
+// that a lane's elements are all inside the row or all outside).
+template <int V>
+__device__ __forceinline__ void pair_rows(const PairArgs& a, const float* tw, int row0, int col, int lane) {
+  const int c = lane % (32 / V) * V;
+  if (col + c >= a.N) return;
+#pragma unroll 4
+  for (int r = lane / (32 / V); r < 32 && row0 + r < a.T; r += V) {
+    const float* f = tw + r * PairCfg::kPad + c;
+    const size_t y = static_cast<size_t>(row0 + r) * a.N + col + c;
+    if (a.y_bf16) {
+      uint16_t* p = static_cast<uint16_t*>(a.Y) + y;
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_word(f[0], f[1]), bf16x2_word(f[2], f[3]));
+      else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = bf16x2_word(f[0], f[1]);
+      else *p = f32_to_bf16_bits(f[0]);
+    } else {
+      float* p = static_cast<float*>(a.Y) + y;
+      if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+      else *p = f[0];
+    }
+  }
+}
+
 // Stores a warp's 32 rows x 32 columns of Y from its registers (v: this lane's row). `turn` counts the warp's
 // TMA stores: a staging half is written again once the store before last (bf16) or the last (fp32) has
 // read it.
@@ -315,20 +338,14 @@ __device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap*
     }
     ++turn;
   } else if (col < a.N) {
-    // through shared memory, a row per store
+    // through shared memory, as many neighbouring elements to a lane as rows of N elements keep aligned
     float* tw = reinterpret_cast<float*>(out);
 #pragma unroll
     for (int i = 0; i < 32; ++i) tw[lane * PairCfg::kPad + i] = __uint_as_float(v[i]);
     __syncwarp();
-    const int rows = min(32, a.T - row0);
-    for (int r = 0; r < rows; ++r) {
-      const float f = tw[r * PairCfg::kPad + lane];
-      if (col + lane < a.N) {
-        const size_t y = static_cast<size_t>(row0 + r) * a.N + col + lane;
-        if (a.y_bf16) static_cast<uint16_t*>(a.Y)[y] = f32_to_bf16_bits(f);
-        else static_cast<float*>(a.Y)[y] = f;
-      }
-    }
+    if (a.y_bf16 && (a.N & 3) == 0) pair_rows<4>(a, tw, row0, col, lane);
+    else if ((a.N & 1) == 0) pair_rows<2>(a, tw, row0, col, lane);
+    else pair_rows<1>(a, tw, row0, col, lane);
     __syncwarp();
   }
 }

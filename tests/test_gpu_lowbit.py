@@ -215,14 +215,17 @@ def product(xc, xs, wc, ws, T, N, dtype):
 # T crosses every token tile; N and K leave ragged tiles, scale tiles and half-filled MMAs
 SHAPES = [(1, 32, 1), (1, 64, 7), (2, 96, 129), (16, 128, 128), (17, 160, 300), (31, 256, 64), (32, 288, 513), (33, 320, 256),
           (64, 352, 200), (65, 384, 130), (100, 416, 1000), (128, 448, 384), (129, 224, 257), (255, 448, 512), (256, 192, 999),
-          (257, 448, 640), (300, 96, 1025), (513, 448, 385), (700, 320, 520), (1100, 448, 777)]
+          (257, 448, 640), (300, 96, 1025), (513, 448, 385), (700, 320, 520), (1100, 448, 777), (300, 64, 1026), (140, 160, 300),
+          # K long enough to be split: over clusters of CTAs, of four pairs and of two pairs
+          (16, 7264, 300), (40, 1568, 520), (200, 7264, 260), (270, 5120, 514), (1030, 5152, 1000), (513, 6208, 2049)]
 
 
 @pytest.mark.parametrize("T,K,N", SHAPES)
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_product_exact(T, K, N, dtype):
-    """Scale exponents in [-1, 1]: every product is a multiple of 2^-4 and every partial sum below 36 * 4 * K <= 2^16, so
-    all sums are exact in fp32 whatever their order, and each row and block must meet its own scale."""
+    """Scale exponents in [-1, 1]: every product is a multiple of 2^-4 and every partial sum at most 36 * 4 * K < 2^20
+    (K < 7281), 24 bits in all, so every sum is exact in fp32 whatever its order, and each row and block must meet its own
+    scale."""
     x, xe, xc, xs, w, we, wc, ws = operands(T, K, N, T + K + N, 1)
     ref = lowbit.mx4_values(x, xe) @ lowbit.mx4_values(w, we).T
     Y = product(xc, xs, wc, ws, T, N, dtype)
@@ -230,7 +233,7 @@ def test_product_exact(T, K, N, dtype):
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 8192, 1024), (16, 8960, 1536), (33, 4096, 520), (128, 2080, 384), (200, 8960, 260),
-                                   (300, 4128, 513), (520, 1536, 1000), (1030, 2048, 2049)])
+                                   (300, 4128, 513), (520, 1536, 1000), (1030, 2048, 2049), (300, 29568, 264), (1030, 8960, 1000)])
 def test_product_long_sums(T, K, N):
     """Wide scales. Products are exact; each of the at most K additions of a sum is off by at most one unit in the last
     place (2^-23) of the magnitudes summed, so |error| <= K * 2^-23 * sum |x w|."""
