@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads)
         pair_store(a, &tm_y, v, row0, n0 + c, lane, out, turn);
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();  // the writes themselves end with the grid
     tc_fence_before();
   }
   __syncthreads();

@@ -182,7 +182,6 @@ template <int n>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 4-byte asynchronous copy global -> shared (no registers involved); completes at cp_async_wait_all().
 __device__ __forceinline__ void cp_async4(void* dst_smem, const void* src) {

@@ -217,7 +217,9 @@ SHAPES = [(1, 32, 1), (1, 64, 7), (2, 96, 129), (16, 128, 128), (17, 160, 300), 
           (64, 352, 200), (65, 384, 130), (100, 416, 1000), (128, 448, 384), (129, 224, 257), (255, 448, 512), (256, 192, 999),
           (257, 448, 640), (300, 96, 1025), (513, 448, 385), (700, 320, 520), (1100, 448, 777), (300, 64, 1026), (140, 160, 300),
           # K long enough to be split: over clusters of CTAs, of four pairs and of two pairs
-          (16, 7264, 300), (40, 1568, 520), (200, 7264, 260), (270, 5120, 514), (1030, 5152, 1000), (513, 6208, 2049)]
+          (16, 7264, 300), (40, 1568, 520), (200, 7264, 260), (270, 5120, 514), (1030, 5152, 1000), (513, 6208, 2049),
+          # more tiles than pairs of CTAs: with a short K, whose activations are kept, and a longer one
+          (2050, 224, 2300), (4900, 1504, 1032), (2310, 1568, 2305)]
 
 
 @pytest.mark.parametrize("T,K,N", SHAPES)
