@@ -407,7 +407,7 @@ QE_API qe_status qe_cooccurrence_npmi(const int32_t* idx, int32_t T, int32_t k, 
  * with a NaN or an infinity gets the scale NaN and codes 0 (int8), or NaN blocks (MXFP4).
  * residual_out may be X or residual, and Y may be X, in place; no other output may overlap an input.
  * Limits: d a multiple of 8 (of 32 for a_bits = 4) and <= 32768, else QE_ERR_UNSUPPORTED; T <= 1<<20;
- * eps >= 0. T = 0 is a no-op.
+ * eps >= 0 (with 0, a row of zeros has no norm and becomes NaN). T = 0 is a no-op.
  */
 QE_API qe_status qe_add_rmsnorm_quant(const void* X, qe_dtype x_dtype, const void* residual, const void* gamma,
                                       qe_dtype gamma_dtype, double eps, int32_t T, int32_t d, const float* s_inv,
@@ -451,8 +451,8 @@ QE_API qe_status qe_mx4_dequantize(const void* codes, const void* scales, int32_
 
 /*
  * Y = X . W^T of an MXFP4 X [T, d_in] and an MXFP4 W [d_out, d_in], on the block-scaled 4-bit tensor cores
- * with fp32 sums, rounded once to y_dtype. Y [T, d_out]. The result is the same from call to call, and a token's row
- * does not depend on the other tokens' values. A NaN scale makes the whole row (X) or column (W) of Y NaN.
+ * with fp32 sums, rounded once to y_dtype. Y [T, d_out], overlapping no operand. The result is the same from call to
+ * call, and a token's row does not depend on the other tokens' values (T decides how the sum over K is split). A NaN scale makes the whole row (X) or column (W) of Y NaN.
  * T = 0 is a no-op. T <= 1<<20, d_out <= 1<<24, d_in as above.
  */
 QE_API qe_status qe_mx4_product(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
