@@ -454,3 +454,159 @@ def test_norm_and_layer_agree_with_the_oracle_layer():
     ref, mag = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
     # integer group sums are exact; K/128 fp32 multiply-adds and the token scale: (K/128 + 3) half steps
     assert (np.abs(out.double().cpu().numpy() - ref) <= (K // 128 + 3) * 2.0 ** -23 * mag).all()
+
+
+# ---------------------------------------------------------------- calls the documentation allows and nothing above makes
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_norm_optional_outputs(bits):
+    """Every output may be left out; what is written does not change."""
+    T, d = 9, 1056
+    x, X = rnd((T, d), 91, BF16)
+    r, R = rnd((T, d), 92, BF16)
+    g = torch.from_numpy(np.random.default_rng(3).standard_normal(d).astype(np.float32)).cuda()
+    s = torch.full((d,), 0.5, device="cuda")
+    H, Y, codes, scales = norm_call(X, R, g, 1e-5, bits, s)
+    for want_y, want_h in ((False, False), (True, False), (False, True)):
+        if bits == 16 and not (want_y or want_h):
+            continue
+        H2, Y2, c2, s2 = norm_call(X, R, g, 1e-5, bits, s, want_y, want_h)
+        assert (Y2 is None) == (not want_y) and (Y2 is None or torch.equal(Y2, Y))
+        assert (H2 is None) == (not want_h) and (H2 is None or torch.equal(H2, H))
+        if bits != 16:
+            assert torch.equal(c2, codes) and torch.equal(s2, scales)
+    _, y, near = lowbit.rmsnorm(x, r, g.cpu().numpy(), 1e-5)[1:]
+    assert not near.any() and np.array_equal(Y.double().cpu().numpy(), rounded(y, BF16))
+
+
+def at16(t):
+    """A copy of t whose address is a multiple of 16 bytes and of no more."""
+    n = t.numel() * t.element_size()
+    buf = torch.empty(n + 64, dtype=torch.uint8, device="cuda")
+    off = (-buf.data_ptr()) % 32 + 16
+    c = buf[off:off + n].view(t.dtype).view(t.shape)
+    c.copy_(t)
+    assert c.data_ptr() % 32 == 16
+    return c
+
+
+@pytest.mark.parametrize("T,K,N", [(5, 1056, 136), (300, 288, 520), (200, 5152, 264)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_least_alignment(T, K, N, dtype):
+    x, xe, xc, xs, w, we, wc, ws = operands(T, K, N, 7, 1)
+    want = product(xc, xs, wc, ws, T, N, dtype)
+    Y = at16(torch.zeros((T, N), dtype=dtype, device="cuda"))
+    qe.mx4_product(at16(xc), at16(xs), at16(wc), at16(ws), Y)
+    assert torch.equal(Y, want)
+    v, V = rnd((T, K), 8, dtype)
+    s = at16(torch.full((K,), 0.75, device="cuda"))
+    codes, scales = quantize(V, s)
+    c2, s2 = at16(torch.zeros_like(codes)), at16(torch.full_like(scales, 0xEE))
+    qe.mx4_quantize(at16(V), c2, s2, s=s)
+    assert torch.equal(c2, codes) and torch.equal(s2, scales)
+    back, b2 = torch.empty((T, K), dtype=dtype, device="cuda"), at16(torch.zeros((T, K), dtype=dtype, device="cuda"))
+    qe.mx4_dequantize(codes, scales, back)
+    qe.mx4_dequantize(c2, s2, b2)
+    assert torch.equal(b2, back)
+    g = torch.ones(K, dtype=dtype, device="cuda")
+    H, Yn, c8, sa = norm_call(V, V, g, 1e-6, 8, s)
+    Y3, c3, s3 = at16(torch.zeros_like(Yn)), at16(torch.zeros_like(c8)), at16(torch.zeros_like(sa))
+    qe.add_rmsnorm_quant(at16(V), at16(g), 1e-6, 8, c3, s3, residual=at16(V), Y=Y3, s_inv=s)
+    assert torch.equal(Y3, Yn) and torch.equal(c3, c8) and torch.equal(s3, sa)
+
+
+def test_very_many_tokens():
+    """2^18 + 77 tokens: more token tiles than any group, over every pair of CTAs."""
+    T, K, N = (1 << 18) + 77, 64, 40
+    g = np.random.default_rng(5)
+    code = torch.randint(0, 256, (T, K // 2), dtype=torch.uint8, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    w = g.integers(0, 16, (N, K)).astype(np.uint8)
+    we = np.full((N, 2), 127, np.uint8)
+    xs = torch.full((qe.mx4_scale_bytes(T, K),), 128, dtype=torch.uint8, device="cuda")
+    Y = product(code, xs, cuda(lowbit.pack_codes(w)), cuda(lowbit.tile_scales(we)), T, N, F32)
+    c = code.cpu().numpy()
+    x = np.stack((c & 15, c >> 4), -1).reshape(T, K)
+    ref = lowbit.mx4_values(x, np.full((T, 2), 128, np.uint8)) @ lowbit.mx4_values(w, we).T
+    assert np.array_equal(Y.double().cpu().numpy(), ref)  # multiples of 1/2 below 2^13: exact
+
+
+@pytest.mark.parametrize("T,N", [(3, 130), (150, 130)])
+def test_very_long_rows(T, N):
+    """K = 2^20 channels, the longest: the last stages count, and only they hold anything."""
+    K, tail = 1 << 20, 4000
+    x, xe, xc, xs, w, we, wc, ws = operands(T, tail // 32 * 32, N, 9, 1)
+    tail = x.shape[1]
+
+    def place(codes, code, e):
+        rows = code.shape[0]
+        full = torch.zeros((rows, K // 2), dtype=torch.uint8, device="cuda")
+        full[:, (K - tail) // 2:] = codes
+        scale = np.full((rows, K // 32), 127, np.uint8)
+        scale[:, (K - tail) // 32:] = e
+        return full, cuda(lowbit.tile_scales(scale))
+
+    Y = product(*place(xc, x, xe), *place(wc, w, we), T, N, F32)
+    ref = lowbit.mx4_values(x, xe) @ lowbit.mx4_values(w, we).T
+    assert np.array_equal(Y.double().cpu().numpy(), ref)
+
+
+def test_many_outputs_with_many_tokens():
+    """2^20 + 131 output channels and 150 tokens: only the first and last channels hold anything."""
+    T, K, N = 150, 64, (1 << 20) + 131
+    x, xe, xc, xs, w, we, wc, ws = operands(T, K, 300, 10, 1)
+    full = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    full[:150], full[-150:] = wc[:150], wc[150:]
+    scale = np.full((N, K // 32), 127, np.uint8)
+    scale[:150], scale[-150:] = we[:150], we[150:]
+    Y = product(xc, xs, full, cuda(lowbit.tile_scales(scale)), T, N, BF16)
+    ref = rounded((lowbit.mx4_values(x, xe) @ lowbit.mx4_values(w, we).T).astype(np.float32), BF16)
+    got = Y.double().cpu().numpy()
+    assert np.array_equal(got[:, :150], ref[:, :150]) and np.array_equal(got[:, -150:], ref[:, 150:])
+    assert not got[:, 150:-150].any()
+
+
+def test_weights_quantized_just_before_they_are_used():
+    """The linear call may read weights early, but not before the call that writes them: alternating weights in one
+    buffer, no synchronization in between."""
+    K, N, T = 4096, 4096, 16
+    Ws = [rnd((N, K), 95 + i, BF16, 0.2)[1] for i in range(2)]
+    X = rnd((T, K), 97, BF16)[1]
+    want = [qe.Mx4Layer.from_float(W).forward(X) for W in Ws]
+    torch.cuda.synchronize()
+    layer = qe.Mx4Layer.from_float(Ws[0])
+    got = []
+    for i in range(30):
+        qe.mx4_quantize(Ws[i % 2], layer.w_codes, layer.w_scales)
+        got.append(layer.forward(X))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+def test_activations_written_just_before_they_are_used():
+    """Norm, product, and the next norm over the same buffers, back to back, many times: each kernel sees what the one
+    before it wrote, and does not overwrite what it still reads."""
+    T, d = 64, 2048
+    W = rnd((d, d), 98, BF16, 0.2)[1]
+    layer = qe.Mx4Layer.from_float(W)
+    g = torch.full((d,), 0.7, dtype=BF16, device="cuda")
+    codes = torch.empty((T, d // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(qe.mx4_scale_bytes(T, d), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        h = rnd((T, d), 99, BF16)[1]
+        y = h.clone()
+        for _ in range(12):
+            qe.add_rmsnorm_quant(y, g, 1e-6, 4, codes, scales, residual=h, residual_out=h)
+            if wait:
+                torch.cuda.synchronize()
+            qe.mx4_product(codes, scales, layer.w_codes, layer.w_scales, y)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return h, y
+
+    slow = chain(True)
+    for _ in range(5):
+        fast = chain(False)
+        assert torch.equal(fast[0], slow[0]) and torch.equal(fast[1], slow[1])
+    assert torch.isfinite(slow[1]).all()
