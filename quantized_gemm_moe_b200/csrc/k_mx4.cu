@@ -89,15 +89,16 @@ __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, siz
 
 template <bool BF16, bool SMOOTH>
 __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const void* __restrict__ X, const float* __restrict__ s,
-                                                                int rows, int cols, int spans, size_t units,
+                                                                int rows, int cols, uint32_t spans, uint32_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
   grid_dep_wait();
   grid_dep_launch();  // a product may set itself up, and load its weights, meanwhile
   const int lane = threadIdx.x & 31;
-  const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t unit = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
-  const size_t pair = unit / spans, row = pair * kQuantRows;
+  const uint32_t pair = unit / spans;  // in 32 bits: a 64-bit division costs as much as a step's arithmetic
+  const size_t row = static_cast<size_t>(pair) * kQuantRows;
   const int span0 = static_cast<int>(unit - pair * spans) * kQuantSpan, k0 = span0 + lane * kLaneK;
   const size_t at = row * cols + k0;
   const uint8_t* x = static_cast<const uint8_t*>(X) + at * (BF16 ? 2 : 4);
@@ -126,16 +127,17 @@ __device__ __forceinline__ float2 e2m1x2(uint32_t c) {
 constexpr int kDequantSpan = 1024;  // channels per warp
 __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, int cols,
-                                                                  int spans, size_t units, void* __restrict__ out,
+                                                                  uint32_t spans, uint32_t units, void* __restrict__ out,
                                                                   int out_bf16) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const size_t unit = blockIdx.x * static_cast<size_t>(kQuantThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t unit = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
-  const size_t row = unit / spans;
+  const uint32_t row32 = unit / spans;
+  const size_t row = row32;
   constexpr int kSteps = kDequantSpan / 256;
-  const int k0 = static_cast<int>(unit - row * spans) * kDequantSpan + lane * 8;
+  const int k0 = static_cast<int>(unit - row32 * spans) * kDequantSpan + lane * 8;
   const size_t base = row * cols;
   const uint8_t* sc = scales + mx_scale_row(row, (cols + kMxTileCols - 1) / kMxTileCols);
   uint32_t c[kSteps], b[kSteps];
@@ -179,10 +181,12 @@ cudaError_t launch_mx4_quantize(const void* X, bool x_bf16, const float* s, int 
   if (rows == 0) return cudaSuccess;
   const int spans = static_cast<int>(ceil_div(cols, kQuantSpan));
   const size_t units = static_cast<size_t>(ceil_div(rows, kQuantRows)) * spans;
+  if (units > 0xFFFF0000u) return cudaErrorInvalidValue;  // four terabytes of bf16
   const unsigned grid = static_cast<unsigned>(ceil_div(units, kQuantThreads / 32));
   auto k = x_bf16 ? (s ? k_mx4_quantize<true, true> : k_mx4_quantize<true, false>)
                   : (s ? k_mx4_quantize<false, true> : k_mx4_quantize<false, false>);
-  return launch_dependent(k, dim3(grid), kQuantThreads, 0, 1, st, X, s, rows, cols, spans, units, codes, scales);
+  return launch_dependent(k, dim3(grid), kQuantThreads, 0, 1, st, X, s, rows, cols, static_cast<uint32_t>(spans), static_cast<uint32_t>(units),
+                          codes, scales);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
@@ -190,8 +194,10 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
   if (rows == 0) return cudaSuccess;
   const int spans = static_cast<int>(ceil_div(cols, kDequantSpan));
   const size_t units = static_cast<size_t>(rows) * spans;
+  if (units > 0xFFFF0000u) return cudaErrorInvalidValue;
   return launch_dependent(k_mx4_dequantize, dim3(static_cast<unsigned>(ceil_div(units, kQuantThreads / 32))), kQuantThreads, 0,
-                          1, st, codes, scales, cols, spans, units, out, static_cast<int>(out_bf16));
+                          1, st, codes, scales, cols, static_cast<uint32_t>(spans), static_cast<uint32_t>(units), out,
+                          static_cast<int>(out_bf16));
 }
 
 }  // namespace qe
