@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kRQThreads) k_route_quant(const RouteQuantArgs
   // A token's wpt warps meet at named barrier 1 + slot when they share its slot sums (wpt >= 2).
   const int gthr = wpt * 32, gtid = sub * 32 + lane;
   auto group_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(gthr) : "memory"); };
-  for (int i = threadIdx.x; i < a.K / 4; i += kRQThreads)
+  for (int i = threadIdx.x; !PRE && i < a.K / 4; i += kRQThreads)
     reinterpret_cast<float4*>(s_inv_s)[i] = __ldg(reinterpret_cast<const float4*>(a.s_inv) + i);
   for (int i = threadIdx.x; i < t1 - t0; i += kRQThreads) mx_s[i] = 0;
   // the decode product's tile counters start at zero (the product runs after this launch)
