@@ -399,11 +399,13 @@ QE_API qe_status qe_cooccurrence_npmi(const int32_t* idx, int32_t T, int32_t k, 
  *   s_inv        (device) fp32 [d], may be NULL: the smoothing factors of the projection
  *   residual_out (device) out [T, d] in X's type, may be NULL (and is when residual is): x + r
  *   Y            (device) out [T, d] in X's type, may be NULL: the normed row
- *   a_bits       8 or 6: codes int8 [T, d] and scales fp32 [T], as qe_act_quant writes them;
+ *   a_bits       8 or 6: codes int8 [T, d] and scales fp32 [T], one per row;
  *                4: codes and scales in MXFP4 (qe_mx4_quantize); 16: no quantized output (codes and
  *                scales are not read and may be NULL; Y or residual_out is then required).
  * Per row: h = fl32(x + r); rstd = fl32(1 / sqrt(sum h^2 / d + eps)) with the sum, root and quotient in
- * fp64; y = fl32(fl32(h * rstd) * gamma); the quantizers read fl32(y * s_inv), not the rounded Y. A row
+ * fp64; y = fl32(fl32(h * rstd) * gamma); the quantizers read v = fl32(y * s_inv), not the rounded Y. int8:
+ * scale = fl32(max|v| * fl32(1/qmax)), qmax = 127 or 31 (within one unit in the last place of qe_act_quant's
+ * fl32(max|v|/qmax)), code = rint(fl32(v/scale)), ties to even; a row of zeros has scale and codes 0. A row
  * with a NaN or an infinity gets the scale NaN and codes 0 (int8), or NaN blocks (MXFP4).
  * residual_out may be X or residual, and Y may be X, in place; no other output may overlap an input.
  * Limits: d a multiple of 8 (of 32 for a_bits = 4) and <= 32768, else QE_ERR_UNSUPPORTED; T <= 1<<20;

@@ -15,6 +15,7 @@ struct NormArgs {
   const float* s_inv;  // or nullptr
   double eps;
   int T, d, qmax, g_bf16;
+  float inv_qmax;      // fl32(1 / qmax)
   void* H;             // x + r in x's type, or nullptr
   void* Y;             // normed row in x's type, or nullptr
   uint8_t* codes;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
   auto codes = [&](size_t row) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, lane < nw ? top_s[lane] : 0u);
     const bool finite = top < 0x7F800000u;
-    const float sa = finite ? __fdiv_rn(__uint_as_float(top), static_cast<float>(a.qmax)) : __uint_as_float(0x7FC00000u);
+    const float sa = finite ? __fmul_rn(__uint_as_float(top), a.inv_qmax) : __uint_as_float(0x7FC00000u);
     if (tid == 0) static_cast<float*>(a.scales)[row] = sa;
     const float inv = sa > 0.0f ? __frcp_rn(sa) : 0.0f;
     const float limit = rtn_fast_ok(sa, inv) ? rtn_limit(a.qmax) : 0.0f;
@@ -303,6 +304,7 @@ cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const 
   a.T = T;
   a.d = d;
   a.qmax = (1 << (a_bits - 1)) - 1;
+  a.inv_qmax = 1.0f / static_cast<float>(a.qmax);
   a.g_bf16 = g_bf16;
   a.H = H;
   a.Y = Y;

@@ -349,16 +349,31 @@ def test_qe_layer_takes_quantized_rows(T, a_bits, xd, K):
     assert qe.device_error() == 0
 
 
-def test_norm_into_qe_layer():
-    """The norm's codes through the layer against the layer's own quantization of the norm's fp32 row: the same codes,
-    because an fp32 Y is not rounded."""
-    T, K = 40, 1536
-    layer = qe_layer(K, 392, 8)
+@pytest.mark.parametrize("bits", [8, 6])
+def test_norm_into_qe_layer(bits):
+    """The norm's codes through the layer, against the layer's quantization of the norm's row (fp32, so that Y is not
+    rounded). The two scales are one unit in the last place apart at most: relative 2^-23. So a code can differ, by one,
+    only where v / scale lies within (qmax + 1) * 2^-22 of a half-integer (both quotients' roundings and the scales'
+    distance); with the layer's own codes and the norm's, everything behind is the same."""
+    T, K = 200, 1536
+    layer = qe_layer(K, 392, bits)
     x, X = rnd((T, K), 51, F32, 0.5)
     r, R = rnd((T, K), 52, F32, 0.5)
     g = torch.ones(K, device="cuda")
-    H, Y, codes, sa = norm_call(X, R, g, 1e-6, 8, layer.s_inv)
-    assert torch.equal(layer.forward_codes(Y, codes, sa), layer.forward(Y))
+    H, Y, codes, sa = norm_call(X, R, g, 1e-6, bits, layer.s_inv)
+    c2, sa2 = torch.empty_like(codes), torch.empty_like(sa)
+    qe.act_quant(Y, layer.s_inv, bits, c2, sa2)
+    assert ((sa - sa2).abs() <= sa * 2.0 ** -23).all()
+    diff = (codes.int() - c2.int()).cpu()
+    assert diff.abs().max() <= 1
+    q = ((Y * layer.s_inv).double() / sa.double()[:, None]).cpu()
+    assert ((q - q.floor() - 0.5).abs()[diff != 0] <= 2 ** (bits - 1) * 2.0 ** -22).all()
+    assert torch.equal(layer.forward_codes(Y, c2, sa2), layer.forward(Y))
+    out, own = layer.forward_codes(Y, codes, sa), layer.forward(Y)
+    same = (diff == 0).all(1).cuda()
+    assert same.any()
+    # rows with equal codes: the product's row scales by sa, the adapters' term is the same; three roundings apart
+    assert torch.allclose(out[same], own[same], rtol=0, atol=float(own.abs().max()) * 2.0 ** -20)
 
 
 # ---------------------------------------------------------------- empty calls, streams, graphs

@@ -72,7 +72,7 @@ def test_oracle_rmsnorm_by_hand():
     assert np.array_equal(h, 2 * x)
     assert rstd[0] == np.float32(1 / np.sqrt(100 / 8)) and y[0, 0] == np.float32(np.float32(6 * rstd[0]) * 2)
     q, sa = lowbit.act_codes(np.array([[1.0, -2.0, 0.5]], np.float32), 6)
-    assert sa[0] == np.float32(2 / 31) and list(q[0]) == [16, -31, 8]  # 15.5 and 7.75: to even, to nearest
+    assert sa[0] == np.float32(2) * np.float32(1 / 31) and list(q[0]) == [16, -31, 8]  # 15.5 and 7.75: to even, to nearest
     q, sa = lowbit.act_codes(np.array([[1.0, np.inf], [0.0, 0.0]], np.float32), 8)
     assert np.isnan(sa[0]) and sa[1] == 0 and not q.any()
 
