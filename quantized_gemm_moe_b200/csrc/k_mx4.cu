@@ -20,7 +20,8 @@ constexpr int kQuantSpan = kStepK * kQuantSteps;      // channels per warp
 // step reads 512 contiguous bytes of bf16 (1 KB of fp32) and writes 128 of codes. All loads of x are in flight
 // before the first is used. HBM: 2 (4) bytes read and 0.53 written for each element; what comes next is L1,
 // which the factors s (1 KB a step) load more than bf16 rows do, hence two rows. 29568 x 8192 bf16 with s:
-// 101 us, 6.1 TB/s (one row and 1024 channels: 111 us).
+// 94 us, 6.5 TB/s with the registers bounded for five CTAs on an SM (101 us with four, 101 with six, which spill; one row
+// and 1024 channels: 111 us).
 // FULL: the warp's channels and rows all exist (nothing is predicated).
 template <bool BF16, bool SMOOTH, bool FULL>
 __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, size_t pitch, const float* __restrict__ s,
@@ -88,7 +89,7 @@ __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, siz
 }
 
 template <bool BF16, bool SMOOTH>
-__global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const void* __restrict__ X, const float* __restrict__ s,
+__global__ void __launch_bounds__(kQuantThreads, 5) k_mx4_quantize(const void* __restrict__ X, const float* __restrict__ s,
                                                                 int rows, int cols, uint32_t spans, uint32_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {

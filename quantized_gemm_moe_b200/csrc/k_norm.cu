@@ -117,7 +117,7 @@ __device__ __forceinline__ void norm_rstd(const double* sum_s, int nw, int lane,
 //   h = fl32(x + r); rstd = fl32(1/sqrt(sum h^2 / d + eps)); y = fl32(fl32(h*rstd)*g); v = fl32(y*s_inv)
 // The sum of squares is held in 64 bits and rstd rounded once, after which every value that decides a
 // code is one fp32 operation, so the codes do not depend on the order of the sum.
-// HBM bound: 8192 x 8192 bf16 with residual, A6: 104 us, 5.8 TB/s; MXFP4: 93 us, 6.1 TB/s. Persistent CTAs that load
+// HBM bound: 8192 x 8192 bf16 with residual, A6: 98 us, 6.2 TB/s; MXFP4: 93 us, 6.1 TB/s. Persistent CTAs that load
 // a row ahead, and several rows to a CTA, were slower (117-136 and 125 us for A6): the registers they take cost
 // more resident warps than they save waits.
 template <bool BF16, int VPT, int OUT>
