@@ -246,17 +246,17 @@ struct PairCfg {
   static constexpr int kEpiWarps = 8;  // two for each 32 token rows, alternate chunks of 32 columns
   static constexpr int kA = 16384, kB = 16384, kSA = 1024, kSB = 2048;
   static constexpr int kStage = kA + kB + kSA + kSB;
-  static constexpr int kStages = 5;
+  // Six stages: 8192 x 1536 -> 8960 52.8 us with five and 49.3 with six, 8192 x 8192 -> 29568 640 and 624.
+  static constexpr int kStages = 6;
   // Tensor memory: two accumulators of 256 columns that share the columns [192, 256), and two sets of scales.
   // The epilogue drains the shared columns first, so the next tile's MMAs start after a quarter of it.
   static constexpr int kAcc1 = 192, kSf = 448, kSfCols = 24;
-  // An epilogue warp's staging buffer: a 32 x 32 block of Y, swizzled for its TMA store (two of them in bf16), or
-  // padded rows of fp32 where Y's rows allow no TMA store.
-  static constexpr int kPad = 33;
-  static constexpr int kOut = 5120;
-  static constexpr int kTrans = kEpiWarps * kOut;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kTrans + 256;
-  static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512 && 32 * kPad * 4 <= kOut, "layout");
+  // An epilogue warp's staging buffer: 32 rows of 64 bytes of Y.
+  static constexpr int kOut = 2048;
+  static constexpr int kStaging = kStages * kStage, kBars = kStaging + kEpiWarps * kOut;
+  // No room to round the base up: dynamic shared memory begins on a multiple of 1024 bytes (the kernel checks).
+  static constexpr size_t kSmem = kBars + 256;
+  static_assert(kStage % 1024 == 0 && kSf + 2 * kSfCols <= 512, "layout");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr int kPairThreads = 64 + 32 * PairCfg::kEpiWarps;
@@ -277,84 +277,87 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& mt, 
   nt = r / rows;
 }
 
-// Stores a warp's 32 x 32 block of Y from padded rows in shared memory, V elements per lane (N a multiple of V, so
-// that a lane's elements are all inside the row or all outside).
-template <int V>
-__device__ __forceinline__ void pair_rows(const PairArgs& a, const float* tw, int row0, int col, int lane) {
-  const int c = lane % (32 / V) * V;
-  if (col + c >= a.N) return;
-#pragma unroll 4
-  for (int r = lane / (32 / V); r < 32 && row0 + r < a.T; r += V) {
-    const float* f = tw + r * PairCfg::kPad + c;
-    const size_t y = static_cast<size_t>(row0 + r) * a.N + col + c;
-    if (a.y_bf16) {
-      uint16_t* p = static_cast<uint16_t*>(a.Y) + y;
-      if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_word(f[0], f[1]), bf16x2_word(f[2], f[3]));
-      else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = bf16x2_word(f[0], f[1]);
-      else *p = f32_to_bf16_bits(f[0]);
-    } else {
-      float* p = static_cast<float*>(a.Y) + y;
-      if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-      else *p = f[0];
-    }
+// Stores 32 rows of 64 bytes of Y by TMA: v is this lane's row (two bf16 or one fp32 to a word). 16-byte pieces are
+// permuted by bits 7-8 of their offset (64-byte swizzle).
+__device__ __forceinline__ void pair_store_tma(const CUtensorMap* tm_y, const uint32_t (&v)[16], int row0, int col, int lane,
+                                               uint8_t* out) {
+  if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
+        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tm_y, out, col, row0);
+    bulk_commit();
   }
 }
-
-// Stores a warp's 32 rows x 32 columns of Y from its registers (v: this lane's row). `turn` counts the warp's
-// TMA stores: a staging half is written again once the store before last (bf16) or the last (fp32) has
-// read it.
-__device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap* tm_y, const uint32_t (&v)[32], int row0,
-                                           int col, int lane, uint8_t* out, int& turn) {
-  if (a.tma) {
-    if (col >= a.N || row0 >= a.T) return;
-    if (a.y_bf16) {
-      // rows of 64 bytes, 16-byte pieces permuted by bits 7-8 of their offset (64-byte swizzle)
-      uint8_t* half = out + (turn & 1) * 2048;
-      if (lane == 0) bulk_wait_read<1>();
-      __syncwarp();
+// Where rows of N elements allow no TMA store: through the same buffer, a row to a store instruction (several rows of
+// less are slower), or four rows of bf16 where they keep 8-byte words aligned. Words are permuted within their row so
+// that neither the lanes' rows nor a row's words meet on a bank. (2048 x 1536 -> 8960: 15.9 us, 8964 18.9, 8961 23.9.)
+__device__ __forceinline__ void pair_store_bf16(const PairArgs& a, const uint32_t (&v)[16], int row0, int col, int lane,
+                                                uint32_t* tw) {
+  const int rows = min(32, a.T - row0), left = a.N - col;  // elements up to the row's end
+  uint16_t* y = static_cast<uint16_t*>(a.Y) + static_cast<size_t>(row0) * a.N + col;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h =
-              __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(half + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(tm_y, half, col, row0);
-        bulk_commit();
-      }
-    } else {
-      // rows of 128 bytes, pieces permuted by bits 7-9 (128-byte swizzle)
-      if (lane == 0) bulk_wait_read<0>();
-      __syncwarp();
+  for (int w = 0; w < 16; ++w) tw[lane * 16 + (w ^ (lane >> 1))] = v[w];
+  __syncwarp();
+  if ((a.N & 3) == 0) {
+    const int w = 2 * (lane & 7);
+    if (2 * w < left) {
+#pragma unroll 4
+      for (int r = lane >> 3; r < rows; r += 4)
+        *reinterpret_cast<uint2*>(y + static_cast<size_t>(r) * a.N + 2 * w) =
+            make_uint2(tw[r * 16 + (w ^ (r >> 1))], tw[r * 16 + ((w + 1) ^ (r >> 1))]);
+    }
+  } else if (lane < left) {
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      y[static_cast<size_t>(r) * a.N + lane] = static_cast<uint16_t>(tw[r * 16 + ((lane >> 1) ^ (r >> 1))] >> (16 * (lane & 1)));
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void pair_store_f32(const PairArgs& a, const uint32_t (&v)[32], int row0, int col, int lane,
+                                               uint32_t* tw) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h, row0 += 16) {  // 16 rows fill the buffer
+    if (lane >> 4 == h) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(out + lane * 128 + (i ^ (lane & 7)) * 16) =
+        *reinterpret_cast<uint4*>(tw + (lane & 15) * 32 + (i ^ (lane & 7)) * 4) =
             make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(tm_y, out, col, row0);
-        bulk_commit();
-      }
     }
-    ++turn;
-  } else if (col < a.N) {
-    // through shared memory, as many neighbouring elements to a lane as rows of N elements keep aligned
-    float* tw = reinterpret_cast<float*>(out);
+    __syncwarp();
+    const int rows = min(16, a.T - row0);
+    uint32_t* y = static_cast<uint32_t*>(a.Y) + static_cast<size_t>(row0) * a.N + col;
+    if (lane < a.N - col) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) y[static_cast<size_t>(r) * a.N + lane] = tw[r * 32 + (lane ^ ((r & 7) * 4))];
+    }
+    __syncwarp();
+  }
+}
+// 32 rows x 32 columns of Y from a warp's accumulator registers.
+__device__ __forceinline__ void pair_store(const PairArgs& a, const CUtensorMap* tm_y, const uint32_t (&v)[32], int row0,
+                                           int col, int lane, uint8_t* out) {
+  if (col >= a.N || row0 >= a.T) return;
+  uint32_t w[16];
+  if (a.y_bf16) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) tw[lane * PairCfg::kPad + i] = __uint_as_float(v[i]);
-    __syncwarp();
-    if (a.y_bf16 && (a.N & 3) == 0) pair_rows<4>(a, tw, row0, col, lane);
-    else if ((a.N & 1) == 0) pair_rows<2>(a, tw, row0, col, lane);
-    else pair_rows<1>(a, tw, row0, col, lane);
-    __syncwarp();
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2_word(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    if (a.tma) pair_store_tma(tm_y, w, row0, col, lane, out);
+    else pair_store_bf16(a, w, row0, col, lane, reinterpret_cast<uint32_t*>(out));
+  } else if (a.tma) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = v[16 * h + i];
+      if (col + 16 * h < a.N) pair_store_tma(tm_y, w, row0, col + 16 * h, lane, out);
+    }
+  } else {
+    pair_store_f32(a, v, row0, col, lane, reinterpret_cast<uint32_t*>(out));
   }
 }
 
@@ -392,10 +395,13 @@ __global__ void __launch_bounds__(kPairThreads)
                const __grid_constant__ CUtensorMap tm_y, const PairArgs a) {
   using C = PairCfg;
   constexpr int NS = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + NS * C::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * C::kStage + C::kTrans);
+  extern __shared__ __align__(1024) uint8_t smem_1k[];
+  uint8_t* smem = smem_1k;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the same in every CTA: all of them leave
+    record_error(a.err, DEVERR_SMEM_BASE);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t* empty = full + NS;
   uint64_t* accf = empty + NS;   // [2] a tile's MMAs are done
   uint64_t* freed = accf + 2;    // the shared columns of a tile are drained (even CTA's, from both CTAs)
@@ -543,8 +549,7 @@ __global__ void __launch_bounds__(kPairThreads)
         }
       }
     }
-    uint8_t* out = staging + (warp - 2) * C::kOut;
-    int turn = 0;
+    uint8_t* out = smem + C::kStaging + (warp - 2) * C::kOut;
     const uint32_t freed0 = mapa(smem_u32(freed), lead);
     int n = 0;
     for (int tile = pair; S == 1 && tile < tiles; tile += pairs, ++n) {
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kPairThreads)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(freed0);
         }
-        pair_store(a, &tm_y, v, row0, n0 + c, lane, out, turn);
+        pair_store(a, &tm_y, v, row0, n0 + c, lane, out);
       }
     }
     if (lane == 0) bulk_wait_read<0>();  // the writes themselves end with the grid

@@ -401,7 +401,7 @@ qe_status mx4_product_impl(const void* x_codes, const void* x_scales, const void
     const bool bf = yd == QE_BF16, tma = (size_t(d_out) * (bf ? 2 : 4)) % 16 == 0;
     CUtensorMap tm_y;
     if (tma && (s = make_tmap(&tm_y, Y, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                              bf ? 2 : 4, d_out, T, 32, 32, bf ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) !=
+                              bf ? 2 : 4, d_out, T, bf ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)) !=
                    QE_OK)
       return s;
     QE_CUDA(launch_mx4_pair(tm_w, tm_x, tm_ws, tm_xs, tma ? &tm_y : nullptr, p, T, d_out, d_in, Y, bf, w_early,

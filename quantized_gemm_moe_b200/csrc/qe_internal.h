@@ -245,7 +245,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 
 // How the MXFP4 product runs. pair: pairs of CTAs over tiles of 256 tokens x 256 output channels, persistent, or one tile
 // to a cluster of `splits` pairs that share its K; all boxes are 128 rows of codes, tm_ws 2 and tm_xs 1 rows of scale
-// tiles, tm_y 32 x 32 elements (null where Y's rows are no multiple of 16 bytes). Otherwise (T <= 128) tiles of 128 output
+// tiles, tm_y 32 rows of 64 bytes (null where Y's rows are no multiple of 16 bytes). Otherwise (T <= 128) tiles of 128 output
 // channels x all tokens, K split over clusters of `splits` CTAs; tm_w boxes are 128 rows, tm_x boxes T rounded up
 // to 16. w_early: the weights may be read before the previous kernel on the stream has ended.
 struct Mx4Plan {

@@ -21,6 +21,7 @@ enum : int {
   DEVERR_WAIT_TEARDOWN = 0x105,
   DEVERR_GRID_BARRIER = 0x106,
   DEVERR_SELFTEST = 0x107,
+  DEVERR_SMEM_BASE = 0x108,  // dynamic shared memory not where the kernel's swizzled layouts need it
 };
 __device__ __forceinline__ void record_error(int* flag, int code) {
   if (flag) atomicCAS(flag, 0, code);
