@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
 
 // ------------------------------------------------------------------ many tokens
 // Y tile of 256 tokens x 256 output channels per pair of CTAs (cta_group::2: each CTA holds 128 token rows, half of
-// the weight rows and a 128 x 256 accumulator), persistent over the tiles. 8192 x 8192 -> 29568: 643 us, 6.2 PFLOP/s or
-// 0.92 of four times the measured bf16 rate (743 us back to back, under the power cap; 1407 us with 128 x 256 tiles
+// the weight rows and a 128 x 256 accumulator), persistent over the tiles. 8192 x 8192 -> 29568: 624 us, 6.4 PFLOP/s or
+// 0.95 of four times the measured bf16 rate (733 us back to back, under the power cap; 1407 us with 128 x 256 tiles
 // of single CTAs). A stage of 256 channels takes 0.28 us while few SMs work and 0.41 us when all do; reading the
 // activations from L2 once for a whole row of tiles left that as it was, so it is the tensor cores' own rate under load.
 // About 6 us of a call are set-up, the first loads and the last tile's stores.
@@ -672,8 +672,8 @@ cudaError_t launch_mx4_pair(const CUtensorMap& tm_w, const CUtensorMap& tm_x, co
   a.m_tiles = p.t_tiles;
   a.n_tiles = p.n_tiles;
   // Token tiles walked together while a tile of weights is in use: as many as keep their activations within 36 MB
-  // of L2, in equal groups, so that the weights are read from HBM once for each group (8192 x 8192 -> 29568, sustained:
-  // 776 us in groups of 8, 743 in one of 32; 8192 x 29568 -> 8192: 766 in groups of 8, 825 in one of 32).
+  // of L2, in equal groups, so that the weights are read from HBM once for each group (8192 x 8192 -> 29568, sustained, with
+  // five stages: 776 us in groups of 8, 743 in one of 32; 8192 x 29568 -> 8192: 766 in groups of 8, 825 in one of 32).
   const int most = static_cast<int>(std::max<int64_t>(1, (int64_t(36) << 20) / (int64_t(256) * K * 17 / 32)));
   a.group = static_cast<int>(ceil_div(p.t_tiles, ceil_div(p.t_tiles, most)));
   a.Y = Y;
