@@ -447,14 +447,16 @@ QE_API size_t qe_mx4_scale_bytes(int32_t rows, int32_t cols); /* 0 on an invalid
 QE_API qe_status qe_mx4_quantize(const void* X, qe_dtype x_dtype, const float* s, int32_t rows, int32_t cols, void* codes,
                                  void* scales, float* s_inv, void* stream);
 
-/* The values of MXFP4 codes, [rows, cols] in fp32 or bf16 (exact in both); NaN where the scale is NaN. */
+/* The values of MXFP4 codes, [rows, cols] in fp32 or bf16 (exact in both for what qe_mx4_quantize writes; infinite beyond
+ * their range); NaN where the scale is NaN. */
 QE_API qe_status qe_mx4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, void* out,
                                    qe_dtype out_dtype, void* stream);
 
 /*
  * Y = X . W^T of an MXFP4 X [T, d_in] and an MXFP4 W [d_out, d_in], on the block-scaled 4-bit tensor cores
  * with fp32 sums, rounded once to y_dtype. Y [T, d_out], overlapping no operand. The result is the same from call to
- * call, and a token's row does not depend on the other tokens' values (T decides how the sum over K is split). A NaN scale makes the whole row (X) or column (W) of Y NaN.
+ * call, and a token's row does not depend on the other tokens' values (T decides how the sum over K is split). A NaN
+ * scale makes the whole row (X) or column (W) of Y NaN.
  * T = 0 is a no-op. T <= 1<<20, d_out <= 1<<24, d_in as above.
  */
 QE_API qe_status qe_mx4_product(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
