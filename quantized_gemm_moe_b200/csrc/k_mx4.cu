@@ -20,11 +20,12 @@ constexpr int kQuantSpan = kStepK * kQuantSteps;      // channels per warp
 // step reads 512 contiguous bytes of bf16 (1 KB of fp32) and writes 128 of codes. All loads of x are in flight
 // before the first is used. HBM: 2 (4) bytes read and 0.53 written for each element; what comes next is L1,
 // which the factors s (1 KB a step) load more than bf16 rows do, hence two rows. 29568 x 8192 bf16 with s:
-// 94 us, 6.5 TB/s with the registers bounded for five CTAs on an SM (101 us with four, 101 with six, which spill; one row
-// and 1024 channels: 111 us).
+// 96 us, 6.4 TB/s with the registers bounded for five CTAs on an SM. (Read through the non-coherent path, which memory
+// that the kernel before may still be writing does not allow, it took 94; there four and six CTAs took 101, and one row
+// and 1024 channels 111.)
 // FULL: the warp's channels and rows all exist (nothing is predicated).
 template <bool BF16, bool SMOOTH, bool FULL>
-__device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, size_t pitch, const float* __restrict__ s,
+__device__ __forceinline__ void quantize_span(const uint8_t* x, size_t pitch, const float* s,
                                               int k0, int cols, int rows, int lane, uint8_t* __restrict__ c,
                                               uint8_t* __restrict__ sc0, uint8_t* __restrict__ sc1) {
   constexpr int kE = BF16 ? 2 : 4;
@@ -36,7 +37,7 @@ __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, siz
       if (FULL || (k0 + kStepK * j < cols && r < rows)) {
 #pragma unroll
         for (int h = 0; h < kE / 2; ++h)
-          raw[j][r][h] = __ldg(reinterpret_cast<const uint4*>(x + r * pitch * kE + kStepK * kE * j) + h);
+          raw[j][r][h] = *(reinterpret_cast<const uint4*>(x + r * pitch * kE + kStepK * kE * j) + h);
       }
     }
   }
@@ -45,8 +46,8 @@ __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, siz
     const int k = k0 + kStepK * j;
     float f[8];
     if (SMOOTH && (FULL || k < cols)) {
-      const float4 f0 = __ldg(reinterpret_cast<const float4*>(s + kStepK * j));
-      const float4 f1 = __ldg(reinterpret_cast<const float4*>(s + kStepK * j) + 1);
+      const float4 f0 = *reinterpret_cast<const float4*>(s + kStepK * j);
+      const float4 f1 = *(reinterpret_cast<const float4*>(s + kStepK * j) + 1);
       f[0] = f0.x; f[1] = f0.y; f[2] = f0.z; f[3] = f0.w;
       f[4] = f1.x; f[5] = f1.y; f[6] = f1.z; f[7] = f1.w;
     }
@@ -89,7 +90,7 @@ __device__ __forceinline__ void quantize_span(const uint8_t* __restrict__ x, siz
 }
 
 template <bool BF16, bool SMOOTH>
-__global__ void __launch_bounds__(kQuantThreads, 5) k_mx4_quantize(const void* __restrict__ X, const float* __restrict__ s,
+__global__ void __launch_bounds__(kQuantThreads, 5) k_mx4_quantize(const void* X, const float* s,
                                                                 int rows, int cols, uint32_t spans, uint32_t units,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
@@ -126,8 +127,8 @@ __device__ __forceinline__ float2 e2m1x2(uint32_t c) {
 // The values of the codes, eight channels per lane and step. Every value has two significant bits, so
 // it is exact in bf16 and fp32 (2^-128, the smallest, is a subnormal of both).
 constexpr int kDequantSpan = 1024;  // channels per warp
-__global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales, int cols,
+__global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t* codes,
+                                                                  const uint8_t* scales, int cols,
                                                                   uint32_t spans, uint32_t units, void* __restrict__ out,
                                                                   int out_bf16) {
   grid_dep_wait();
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const uint8_t*
   for (int j = 0; j < kSteps; ++j) {
     const int k = k0 + 256 * j;
     if (k < cols) {
-      c[j] = __ldg(reinterpret_cast<const uint32_t*>(codes + (base + k) / 2));
-      b[j] = __ldg(sc + mx_scale_at(k));
+      c[j] = *reinterpret_cast<const uint32_t*>(codes + (base + k) / 2);
+      b[j] = sc[mx_scale_at(k)];
     }
   }
 #pragma unroll

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
 
 // out[t][k] = codes[t][k] * sa[t], eight channels per thread and step, four steps in flight.
 constexpr int kDequantSteps = 4;
-__global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ codes, const float* __restrict__ sa,
+__global__ void __launch_bounds__(256) k_act_dequant(const int8_t* codes, const float* sa,
                                                      uint32_t d8, uint32_t n8, void* __restrict__ out, int out_bf16) {
   grid_dep_wait();
   grid_dep_launch();
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(256) k_act_dequant(const int8_t* __restrict__ 
   for (int j = 0; j < kDequantSteps; ++j) {
     const uint32_t i = i0 + 256u * j;
     if (i < n8) {
-      w[j] = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-      s[j] = __ldg(sa + i / d8);
+      w[j] = *(reinterpret_cast<const uint2*>(codes) + i);
+      s[j] = sa[i / d8];
     }
   }
 #pragma unroll

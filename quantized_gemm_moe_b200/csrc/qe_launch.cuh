@@ -10,6 +10,8 @@ namespace qe {
 // another kernel reads or writes, each of its threads that does waits in grid_dep_wait() for that kernel, and
 // with it everything earlier, to have ended. It calls grid_dep_launch() only after that wait, so a kernel
 // that begins behind it finds all work before it done.
+// Its inputs may still be written while it is resident, so it reads them with ordinary loads behind the wait: no
+// non-coherent load (__ldg, or what the compiler makes of a const __restrict__ pointer) is ordered behind anything.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
                              Args&&... args) {
