@@ -404,9 +404,10 @@ QE_API qe_status qe_cooccurrence_npmi(const int32_t* idx, int32_t T, int32_t k, 
  *                scales are not read and may be NULL; Y or residual_out is then required).
  * Per row: h = fl32(x + r); rstd = fl32(1 / sqrt(sum h^2 / d + eps)) with the sum, root and quotient in
  * fp64; y = fl32(fl32(h * rstd) * gamma); the quantizers read v = fl32(y * s_inv), not the rounded Y. int8:
- * scale = fl32(max|v| * fl32(1/qmax)), qmax = 127 or 31 (within one unit in the last place of qe_act_quant's
- * fl32(max|v|/qmax)), code = rint(fl32(v/scale)), ties to even; a row of zeros has scale and codes 0. A row
- * with a NaN or an infinity gets the scale NaN and codes 0 (int8), or NaN blocks (MXFP4).
+ * scale = fl32(max|v| / qmax), qmax = 127 or 31, code = rint(fl32(v/scale)), ties to even; a row of zeros has
+ * scale and codes 0. These are qe_act_quant's of an fp32 Y, so qe_linear_forward_codes gives what
+ * qe_linear_forward gives for that Y, bit for bit. A row with a NaN or an infinity gets the scale NaN and
+ * codes 0 (int8), or NaN blocks (MXFP4).
  * residual_out may be X or residual, and Y may be X, in place; no other output may overlap an input.
  * Limits: d a multiple of 8 (of 32 for a_bits = 4) and <= 32768, else QE_ERR_UNSUPPORTED; T <= 1<<20;
  * eps >= 0 (with 0, a row of zeros has no norm and becomes NaN). T = 0 is a no-op.

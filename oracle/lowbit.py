@@ -82,12 +82,12 @@ def rmsnorm(x: np.ndarray, r, gamma: np.ndarray, eps: float):
 
 
 def act_codes(v: np.ndarray, bits: int):
-    """Per-row symmetric integer codes int8 and scales fl32(max|v| * fl32(1/qmax)) of fp32 v; a row that is not
+    """Per-row symmetric integer codes int8 and scales fl32(max|v| / qmax) of fp32 v; a row that is not
     finite: NaN and 0."""
     qmax = np.float32(2 ** (bits - 1) - 1)
     ok = np.isfinite(v).all(-1)
     w = np.where(ok[:, None], v, np.float32(0)).astype(np.float32)
-    sa = (np.abs(w).max(-1) * (np.float32(1) / qmax)).astype(np.float32)
+    sa = (np.abs(w).max(-1) / qmax).astype(np.float32)
     with np.errstate(all="ignore"):
         q = np.rint((w / sa[:, None]).astype(np.float32))
     q = np.where(sa[:, None] > 0, np.clip(q, -qmax, qmax), 0).astype(np.int8)

@@ -15,7 +15,6 @@ struct NormArgs {
   const float* s_inv;  // or nullptr
   double eps;
   int T, d, qmax, g_bf16;
-  float inv_qmax;      // fl32(1 / qmax)
   void* H;             // x + r in x's type, or nullptr
   void* Y;             // normed row in x's type, or nullptr
   uint8_t* codes;
@@ -117,7 +116,7 @@ __device__ __forceinline__ void norm_rstd(const double* sum_s, int nw, int lane,
 //   h = fl32(x + r); rstd = fl32(1/sqrt(sum h^2 / d + eps)); y = fl32(fl32(h*rstd)*g); v = fl32(y*s_inv)
 // The sum of squares is held in 64 bits and rstd rounded once, after which every value that decides a
 // code is one fp32 operation, so the codes do not depend on the order of the sum.
-// HBM bound: 8192 x 8192 bf16 with residual, A6: 98 us, 6.2 TB/s; MXFP4: 93 us, 6.1 TB/s. Persistent CTAs that load
+// HBM bound: 8192 x 8192 bf16 with residual, A6: 99 us, 6.1 TB/s; MXFP4: 95 us, 6.0 TB/s. Persistent CTAs that load
 // a row ahead, and several rows to a CTA, were slower (117-136 and 125 us for A6): the registers they take cost
 // more resident warps than they save waits.
 template <bool BF16, int VPT, int OUT>
@@ -203,11 +202,11 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const NormArgs a) {
       }
     }
   };
-  // the int8 codes of a row
+  // the int8 codes of a row, with the scale of the layer's own quantization: the two give the same codes
   auto codes = [&](size_t row) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, lane < nw ? top_s[lane] : 0u);
     const bool finite = top < 0x7F800000u;
-    const float sa = finite ? __fmul_rn(__uint_as_float(top), a.inv_qmax) : __uint_as_float(0x7FC00000u);
+    const float sa = finite ? __fdiv_rn(__uint_as_float(top), static_cast<float>(a.qmax)) : __uint_as_float(0x7FC00000u);
     if (tid == 0) static_cast<float*>(a.scales)[row] = sa;
     const float inv = sa > 0.0f ? __frcp_rn(sa) : 0.0f;
     const float limit = rtn_fast_ok(sa, inv) ? rtn_limit(a.qmax) : 0.0f;
@@ -304,7 +303,6 @@ cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const 
   a.T = T;
   a.d = d;
   a.qmax = (1 << (a_bits - 1)) - 1;
-  a.inv_qmax = 1.0f / static_cast<float>(a.qmax);
   a.g_bf16 = g_bf16;
   a.H = H;
   a.Y = Y;
