@@ -346,14 +346,21 @@ def _rows(t, name: str):
     return t.shape
 
 
-def _on(stream):
-    """What is allocated inside belongs to the stream the call runs on (a torch stream or a raw handle),
-    so the allocator never hands it to another stream, or out of a graph's capture, while it is in use."""
+def _external(handle: int, like):
+    import torch
+    _need_cuda(like)
+    return torch.cuda.ExternalStream(handle, device=like.device)
+
+
+def _on(stream, like):
+    """What is allocated inside belongs to the stream the call runs on (a torch stream, or a raw handle of the
+    device of `like`), so the allocator never hands it to another stream, or out of a graph's capture, while it is
+    in use."""
     import contextlib
     import torch
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _external(int(stream), like))
 
 
 def _scratch(shape, dtype, like):
@@ -507,7 +514,7 @@ class QELayer:
     def forward_codes(self, X, codes, sa, out_dtype=None, Y=None, stream=None):
         """forward for rows that are already quantized (add_rmsnorm_quant with this layer's s_inv and a_bits)."""
         T = X.shape[0]
-        with _on(stream):
+        with _on(stream, X):
             Y = _scratch((T, self.desc.d_out), out_dtype or X.dtype, X) if Y is None else Y
             ws = _scratch((max(256, linear_workspace_bytes(self.desc, T)),), None, X)
             linear_forward_codes(self.desc, self.weights, X, codes, sa, Y, ws, stream)
@@ -531,7 +538,7 @@ class Mx4Layer:
         input by their reciprocals."""
         import torch
         N, K = _rows(W, "W")
-        with _on(stream):
+        with _on(stream, W):
             codes = _scratch((N, K // 2), None, W)
             scales = _scratch((mx4_scale_bytes(N, K),), None, W)
             s_inv = None if s is None else _scratch((K,), torch.float32, W)
@@ -540,7 +547,7 @@ class Mx4Layer:
 
     def forward(self, X, out_dtype=None, Y=None, stream=None):
         T = _rows(X, "X")[0]
-        with _on(stream):
+        with _on(stream, X):
             Y = _scratch((T, self.d_out), out_dtype or X.dtype, X) if Y is None else Y
             ws = _scratch((mx4_linear_workspace_bytes(T, self.d_in),), None, X)
             mx4_linear_forward(self.w_codes, self.w_scales, X, Y, ws, self.s_inv, stream)
@@ -548,7 +555,7 @@ class Mx4Layer:
 
     def forward_codes(self, codes, scales, out_dtype=None, Y=None, stream=None):
         import torch
-        with _on(stream):
+        with _on(stream, codes):
             if Y is None:
                 Y = _scratch((_rows(codes, "codes")[0], self.d_out), out_dtype or torch.bfloat16, codes)
             mx4_product(codes, scales, self.w_codes, self.w_scales, Y, stream)
