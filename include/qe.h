@@ -419,7 +419,7 @@ QE_API qe_status qe_add_rmsnorm_quant(const void* X, qe_dtype x_dtype, const voi
 
 /*
  * The values of per-token int8 codes (qe_act_quant, qe_add_rmsnorm_quant): out[t][k] = codes[t][k]*sa[t],
- * fp32, or rounded once to bf16. d_in a multiple of 8.
+ * fp32, or rounded once to bf16. d_in a multiple of 8 and <= 1<<20, else QE_ERR_UNSUPPORTED; T <= 1<<20.
  */
 QE_API qe_status qe_act_dequant(const int8_t* codes, const float* sa, int32_t T, int32_t d_in, void* out,
                                 qe_dtype out_dtype, void* stream);

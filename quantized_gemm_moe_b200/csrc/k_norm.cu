@@ -1,5 +1,7 @@
 // The residual's addition and the root-mean-square norm in front of a quantized projection, with the
 // normed row quantized in the same pass, and the dequantization of per-token int8 codes.
+#include <algorithm>
+
 #include "qe_internal.h"
 #include "qe_launch.cuh"
 #include "qe_ptx.cuh"
@@ -314,11 +316,19 @@ cudaError_t launch_add_rmsnorm(const void* X, bool x_bf16, const void* R, const 
 
 cudaError_t launch_act_dequant(const int8_t* codes, const float* sa, int T, int d, void* out, bool out_bf16,
                                cudaStream_t st) {
-  const size_t n8 = static_cast<size_t>(T) * (d / 8);
-  if (n8 == 0) return cudaSuccess;
-  if (n8 > 0xFFFF0000u) return cudaErrorInvalidValue;  // 32 G elements
-  return launch_dependent(k_act_dequant, dim3(static_cast<unsigned>(ceil_div(n8, 256 * kDequantSteps))), 256, 0, 1, st, codes, sa,
-                          static_cast<uint32_t>(d / 8), static_cast<uint32_t>(n8), out, static_cast<int>(out_bf16));
+  // the kernel counts vectors of eight in 32 bits: larger matrices go in ranges of rows
+  const uint32_t d8 = static_cast<uint32_t>(d / 8);
+  const int most = static_cast<int>(std::min<uint32_t>(0xFFFF0000u / d8, 1u << 30));
+  for (int row = 0; row < T; row += std::min(most, T - row)) {
+    const uint32_t n8 = static_cast<uint32_t>(std::min(most, T - row)) * d8;
+    const size_t at = static_cast<size_t>(row) * d;
+    const cudaError_t e = launch_dependent(k_act_dequant, dim3(static_cast<unsigned>(ceil_div(n8, 256 * kDequantSteps))), 256, 0,
+                                           1, st, codes + at, sa + row, d8, n8,
+                                           static_cast<void*>(static_cast<uint8_t*>(out) + at * (out_bf16 ? 2 : 4)),
+                                           static_cast<int>(out_bf16));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace qe

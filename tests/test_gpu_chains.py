@@ -81,3 +81,22 @@ def test_product_and_quantization_in_turn(T, d, dtype):
         return out + [y]
 
     agree(chain)
+
+
+def test_values_of_the_largest_rows_and_the_most_tokens():
+    """2^20 tokens of 32768 channels, the most the norm writes: 2^32 vectors of eight channels."""
+    T, d = 1 << 20, 32768
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 115 << 30:
+        pytest.skip("needs 103 GB")
+    codes = torch.full((T, d), 3, dtype=torch.int8, device="cuda")
+    sa = (torch.arange(T, device="cuda") % 61 + 1).float()
+    out = torch.full((T, d), -1.0, dtype=BF16, device="cuda")
+    codes[-5:, :] = 1
+    qe.act_dequant(codes, sa, out)
+    want = 3 * sa  # at most 183: exact in bf16
+    want[-5:] = sa[-5:]
+    for t in range(0, T, 1 << 14):
+        assert (out[t:t + (1 << 14)] == want[t:t + (1 << 14), None]).all()
+    del codes, out
+    torch.cuda.empty_cache()
