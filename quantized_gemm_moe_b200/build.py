@@ -21,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqe.so")
 BINDING_SRC = os.path.join(CSRC, "qe_torch.cpp")
 BINDING = os.path.join(HERE, "_qe_torch.so")
+BINDING_ABI = os.path.join(HERE, "_build", "qe_torch.abi")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -48,9 +49,24 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
+def _binding_abi() -> str:
+    """What the module's binary interface hangs on: it calls torch's C++ and Python's C interface."""
+    import sysconfig
+    import torch
+    return f"torch {torch.__version__} cxx11 {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}\n"
+
+
+def binding_up_to_date() -> bool:
+    """Newer than its sources, and built for the torch and the Python that would load it."""
+    if not _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "qe.h")]) or not os.path.exists(BINDING_ABI):
+        return False
+    with open(BINDING_ABI) as f:
+        return f.read() == _binding_abi()
+
+
 def build_binding(force: bool = False) -> str:
     """g++ against torch's headers; libqe.so is found next to the module."""
-    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "qe.h")]):
+    if not force and binding_up_to_date():
         return BINDING
     import sysconfig
     import torch
@@ -68,6 +84,9 @@ def build_binding(force: bool = False) -> str:
         sys.stdout.write(r.stdout.decode(errors="replace"))
         raise RuntimeError("g++ failed for " + BINDING_SRC)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_ABI), exist_ok=True)
+    with open(BINDING_ABI, "w") as f:
+        f.write(_binding_abi())
     return BINDING
 
 
