@@ -701,6 +701,7 @@ qe_status qe_add_rmsnorm_quant(const void* X, qe_dtype x_dtype, const void* resi
   if (!gamma) return QE_ERR_INVALID_ARG;
   if (T == 0) return QE_OK;
   if (a_bits == 16 && !Y && !residual_out) return QE_ERR_INVALID_ARG;
+  if (Y && Y == residual_out) return QE_ERR_INVALID_ARG;
   if (!X || (a_bits != 16 && (!codes || !scales))) return QE_ERR_INVALID_ARG;
   for (const void* p : {X, residual, gamma, static_cast<const void*>(s_inv), static_cast<const void*>(residual_out),
                         static_cast<const void*>(Y), static_cast<const void*>(codes), static_cast<const void*>(scales)})
