@@ -408,8 +408,8 @@ QE_API qe_status qe_cooccurrence_npmi(const int32_t* idx, int32_t T, int32_t k, 
  * scale and codes 0. These are qe_act_quant's of an fp32 Y, so qe_linear_forward_codes gives what
  * qe_linear_forward gives for that Y, bit for bit. A row with a NaN or an infinity gets the scale NaN and
  * codes 0 (int8), or NaN blocks (MXFP4).
- * residual_out may be X or residual, or Y may be X, in place; no other output may overlap an input, and no two
- * outputs one another (Y = residual_out -> QE_ERR_INVALID_ARG).
+ * residual_out may be X or residual, and Y may be X, in place, but not both the same buffer (Y = residual_out ->
+ * QE_ERR_INVALID_ARG); no other output may overlap an input, and no output another.
  * Limits: d a multiple of 8 (of 32 for a_bits = 4) and <= 32768, else QE_ERR_UNSUPPORTED; T <= 1<<20;
  * eps >= 0 (with 0, or one so small that fl32(1/sqrt(eps)) is infinite, a row of zeros becomes NaN). T = 0 is a no-op.
  */

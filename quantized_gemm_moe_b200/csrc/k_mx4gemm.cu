@@ -237,11 +237,12 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx4_split(const __grid_consta
 
 // ------------------------------------------------------------------ many tokens
 // Y tile of 256 tokens x 256 output channels per pair of CTAs (cta_group::2: each CTA holds 128 token rows, half of
-// the weight rows and a 128 x 256 accumulator), persistent over the tiles. 8192 x 8192 -> 29568: 624 us, 6.4 PFLOP/s or
-// 0.95 of four times the measured bf16 rate (733 us back to back, under the power cap; 1407 us with 128 x 256 tiles
-// of single CTAs). A stage of 256 channels takes 0.28 us while few SMs work and 0.41 us when all do; reading the
-// activations from L2 once for a whole row of tiles left that as it was, so it is the tensor cores' own rate under load.
-// About 6 us of a call are set-up, the first loads and the last tile's stores.
+// the weight rows and a 128 x 256 accumulator), persistent over the tiles. 8192 x 8192 -> 29568: 637 us (624 to
+// 652 from one GPU to another), 6.2 PFLOP/s or 0.93 of four times the measured bf16 rate (733 to 773 us back to back, under
+// the power cap; 1407 us with 128 x 256 tiles of single CTAs). A stage of 256 channels takes 0.29 us while one pair works
+// and 0.37 us on average in that product, where a pair runs 1632 (296 tiles on 74 pairs: 0.33 us between K = 1536 and
+// 4608, 0.39 to 0.41 beyond). Reading the activations from L2 once for a whole row of tiles left the time as it was, so
+// L2 is not what makes the difference. About 6 us of a call are set-up, the first loads and the last tile's stores.
 struct PairCfg {
   static constexpr int kEpiWarps = 8;  // two for each 32 token rows, alternate chunks of 32 columns
   static constexpr int kA = 16384, kB = 16384, kSA = 1024, kSB = 2048;
@@ -298,7 +299,7 @@ __device__ __forceinline__ void pair_store_tma(const CUtensorMap* tm_y, const ui
 }
 // Where rows of N elements allow no TMA store: through the same buffer, a row to a store instruction (several rows of
 // less are slower), or four rows of bf16 where they keep 8-byte words aligned. Words are permuted within their row so
-// that neither the lanes' rows nor a row's words meet on a bank. (2048 x 1536 -> 8960: 15.9 us, 8964 18.9, 8961 23.9.)
+// that neither the lanes' rows nor a row's words meet on a bank. (2048 x 1536 -> 8960: 16.4 us, 8964 19.0, 8961 24.0.)
 __device__ __forceinline__ void pair_store_bf16(const PairArgs& a, const uint32_t (&v)[16], int row0, int col, int lane,
                                                 uint32_t* tw) {
   const int rows = min(32, a.T - row0), left = a.N - col;  // elements up to the row's end
@@ -631,8 +632,8 @@ int resident_clusters() {
 }  // namespace
 
 // Up to 128 tokens a tile's MMAs have as many columns as there are tokens, and the split kernel streams weights
-// through all SMs; above, 256 x 256 tiles load less for each product (130 x 4096 -> 6144: 10.7 us, and 11.5 with
-// 144-column tiles; 256 x 8192 -> 8192: 15.6 and 17.8).
+// through all SMs; above, 256 x 256 tiles load less for each product (130 x 4096 -> 6144, bf16: 10.7 us, and 11.5 with
+// 144-column tiles; 256 x 8192 -> 8192: 15.6 and 17.8; both with five stages. With six 10.6 and 14.2).
 Mx4Plan plan_mx4(int T, int N, int K) {
   Mx4Plan p{};
   int sms = decode_grid_sms();
@@ -644,7 +645,7 @@ Mx4Plan plan_mx4(int T, int N, int K) {
     p.n_tiles = static_cast<int>(ceil_div(N, 256));
     p.t_tiles = static_cast<int>(ceil_div(T, 256));
     const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.t_tiles;
-    // K slices where the tiles leave SMs idle and a slice's saving (0.28 us a stage) exceeds the 2 to 3 us that the
+    // K slices where the tiles leave SMs idle and a slice's saving (0.29 us a stage) exceeds the 2 to 3 us that the
     // larger cluster and its sum cost: 512 x 8192 -> 1024: 15.0, 12.8 and 11.5 us with 1, 2 and 4 slices;
     // 512 x 4096 -> 4096: 10.9 and 11.7 with 1 and 2
     if (stages >= 20) {

@@ -280,7 +280,9 @@ cudaError_t launch_norm_t(const NormArgs& a, int out, cudaStream_t st) {
 // vectors, up to 1024 (300 x 4096 int8: 5.4 us against 6.0 with two). With more rows, fewer and fatter warps pay
 // less for the block reductions and keep as many bytes in flight (8192 x 8192 bf16 A6: 201 us with one vector,
 // 127 with two, 104 with four, 118 with eight at half the warps; 4096 x 4096: 38, 31, 32); fp32 rows have twice
-// the bytes for the same work and stop at two (4096 x 8192: 98 us, and 110 with four).
+// the bytes for the same work and take two up to 8192 channels (4096 x 8192: 98 us, and 110 with four). Longer ones take four,
+// for which 64 registers are too few in fp32 (68 to 104 bytes a thread in local memory): 300 x 8960 9.6 us, 4096 x 12288 162.
+// bf16 rows near the longest leave one CTA on an SM, and its waits show: 2000 x 29568 119 us, 5.0 TB/s.
 template <bool BF16>
 cudaError_t launch_norm_x(const NormArgs& a, int out, cudaStream_t st) {
   const int vecs = a.d / 8;
